@@ -54,7 +54,8 @@ typedef enum {
     SAGE_ERR_WORKSPACE_TOO_SMALL = 5,
     SAGE_ERR_CUDA = 6,                 /* a CUDA runtime/driver call failed */
     SAGE_ERR_TIMEOUT = 7,              /* a bounded in-kernel wait gave up */
-    SAGE_ERR_MISALIGNED = 8            /* a pointer is not 16-byte aligned */
+    SAGE_ERR_MISALIGNED = 8,           /* a pointer is not 16-byte aligned */
+    SAGE_ERR_BAD_PAGE = 9              /* a kernel met a page number or a length outside the cache */
 } sage_status;
 
 typedef enum { SAGE_BF16 = 0, SAGE_FP16 = 1 } sage_dtype;
@@ -192,8 +193,9 @@ SAGE_API sage_status sage_debug_qk_int32(const sage_quant_view *view, const sage
                                 int32_t *out_128x128, void *stream);
 
 /*
- * Returns the first device-side error recorded since the last call
- * (SAGE_OK or SAGE_ERR_TIMEOUT) and clears it.  Synchronises `stream`.
+ * Returns the device-side error recorded since the last call and clears it:
+ * SAGE_OK, SAGE_ERR_TIMEOUT, or (no wait gave up) SAGE_ERR_BAD_PAGE from the
+ * paged-cache entry points.  Synchronises `stream`.
  */
 SAGE_API sage_status sage_last_device_error(void *stream);
 
@@ -380,6 +382,148 @@ SAGE_API sage_status sage_debug_kv_quant_two_pass(int32_t on);
  * 4 s).  Synchronises `stream`.  1 <= timeout_us <= 10 s, or 0.
  */
 SAGE_API sage_status sage_debug_wait_limit(uint32_t timeout_us, void *stream);
+
+/*
+ * ------------------------------------------------------------ serving: paged
+ * key-value cache, attention of one new token, sliding-window attention
+ *
+ * Visibility, for a query at position p and a key at position j of its sequence:
+ *   j <= p  and  (window == 0  or  p - j < window  or  j < sinks)
+ * i.e. causal, the last `window` keys (the query's own among them), and the
+ * first `sinks` tokens, which stay visible.  window == 0: no window.
+ * Outputs must not overlap inputs; tables, lengths, log-sum-exps and weights
+ * need the alignment of their type alone.
+ */
+
+/*
+ * A pool of pages.  The keys and values of token t of sequence b are in page
+ * table[b, t / page_size], row t % page_size.  Quantised caches hold INT8 keys
+ * and E4M3 values with one fp32 scale per (token, head) each:
+ * K = k_scale * code (+ km, see sage_kv_append), V = v_scale * code.
+ */
+typedef struct {
+    int32_t Hkv, d;        /* key/value heads, head_dim (64 or 128) */
+    int32_t dtype;         /* sage_dtype of the tokens' K, V, Q and O, and of a 16-bit cache */
+    int32_t quantized;     /* 0: pages of p->dtype; 1: INT8 keys, E4M3 values */
+    int32_t page_size;     /* tokens a page: a power of two, 16 to 1024 */
+    int32_t n_pages;       /* pages in the pool */
+    int32_t layout;        /* SAGE_HND: pages [n_pages, Hkv, page_size, d]; SAGE_NHD: [n_pages, page_size, Hkv, d] */
+    void  *k_pages, *v_pages;
+    float *k_scale, *v_scale;  /* [n_pages, Hkv, page_size] in either layout; NULL unless quantized */
+    float *weight;         /* [n_pages, Hkv, page_size]: attention weight each cached token has gathered
+                              (sage_attn_decode adds to it, sage_kv_evict goes by it), or NULL */
+} sage_kv_cache;
+
+/* The sequences of a call. */
+typedef struct {
+    int32_t B;             /* sequences, at most 65535 */
+    int32_t max_pages;     /* page-table entries a sequence (max_pages * page_size < 2^30 tokens) */
+    const int32_t *table;  /* device [B, max_pages]: page numbers; entries no call looks up may hold anything */
+    const int32_t *lens;   /* device [B]: tokens that the cache holds */
+} sage_kv_seqs;
+
+/*
+ * What the kernels below do with device data that is out of bounds: a page
+ * number outside [0, n_pages) counts as a page without tokens (nothing is read
+ * from it or written to it), a length outside [0, max_pages * page_size] is
+ * taken as the nearest bound; both record SAGE_ERR_BAD_PAGE for
+ * sage_last_device_error.  Two sequences of a call may share pages that the
+ * call only reads.  Only looked-up table entries are read: those of the visible
+ * keys (sage_attn_decode), of the new tokens (sage_kv_append).
+ */
+
+/*
+ * Writes new tokens into the cache: token i < n_new[b] of sequence b goes to
+ * position lens[b] + i.  k, v: device [B, Hkv, T, d] (SAGE_HND) or
+ * [B, T, Hkv, d] (SAGE_NHD), in c->dtype; rows i >= n_new[b] are not read.
+ * n_new: device [B], values in [0, T], or NULL (T for every sequence).  s->lens
+ * is not changed: the caller adds n_new before attending.  Tokens past
+ * max_pages * page_size are dropped and SAGE_ERR_BAD_PAGE is recorded.
+ *   16-bit cache: copies.
+ *   quantized:    x = K - km (fp32; km NULL: K), k_scale = max|x| / 127,
+ *                 code = clamp(rint(x / k_scale), -127, 127);
+ *                 v_scale = max|V| / 448, code = E4M3_rn_satfinite(V / v_scale)
+ *                 (IEEE fp32 divisions; a scale of 0 gives codes 0; a NaN makes
+ *                 its row's scale NaN).
+ * km: device fp32 [B, Hkv, d] or NULL: a per-channel mean that the keys of a
+ * sequence are stored without (view->km of the prefill).  A constant shift of
+ * all keys leaves the softmax as it is, so sage_attn_decode needs km for the
+ * log-sum-exp alone.  Only with a quantized cache.
+ * c->weight of a new token (if any) becomes 0.
+ */
+SAGE_API sage_status sage_kv_append(const void *k, const void *v, const int32_t *n_new, const float *km, int32_t T,
+                                    int32_t layout, const sage_kv_cache *c, const sage_kv_seqs *s, void *stream);
+
+typedef struct {
+    int32_t Hq;            /* query heads, a multiple of c->Hkv */
+    int32_t window, sinks; /* see the visibility above; >= 0 */
+    float   sm_scale;      /* <= 0 selects 1/sqrt(d) */
+} sage_decode_params;
+
+/* Bytes of workspace that sage_attn_decode needs (0: invalid arguments).  Goes by sizes, c->weight != NULL and
+ * max_pages alone (device data and lengths do not matter). */
+SAGE_API size_t sage_decode_workspace_bytes(const sage_kv_cache *c, const sage_kv_seqs *s,
+                                            const sage_decode_params *p);
+
+/*
+ * Attention of one new token a sequence over its cached keys and values: the
+ * query is at position lens[b] - 1 (its own key has been appended).
+ *   S_j = sm_scale q . K_j over the visible j, lse = ln sum_j exp(S_j),
+ *   o = sum_j exp(S_j - lse) V_j
+ * q, o: device [B, Hq, d] in c->dtype; lse: device fp32 [B, Hq] or NULL.  With
+ * lens[b] == 0: o = 0 and lse = -infinity.  km (device fp32 [B, Hkv, d] or
+ * NULL; quantized caches): lse += sm_scale q . km, for the keys as they were
+ * before km was taken off.  With c->weight, every visible key's weight grows by
+ * sum over the query heads of its group of exp(S_j - lse); sequences of one call
+ * must not share pages then.
+ * Softmax statistics and sums are held in fp32; the weights of V enter the
+ * tensor cores as two 16-bit numbers that together carry 16 bits or more.
+ * Results do not depend on scheduling (no atomics): the same inputs give the
+ * same bytes.
+ */
+SAGE_API sage_status sage_attn_decode(const void *q, void *o, float *lse, const float *km, const sage_kv_cache *c,
+                                      const sage_kv_seqs *s, const sage_decode_params *p, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+/*
+ * Eviction by gathered attention weight.  For each (b, kv head), n = lens[b]:
+ *   n <= keep: every token stays;
+ *   n > keep:  the first `sinks`, the last `recent`, and of the others the
+ *              keep - sinks - recent with the largest weight (equal weights: the
+ *              earlier token; NaN counts as lighter than every number).
+ * The tokens that stay move, in their order, to positions 0, 1, ... of the pages
+ * dst_table[b, :] (device [B, dst_pages], dst_pages * page_size >= keep), K, V,
+ * scales and weights; the pages of s->table keep what they hold.  A page of
+ * dst_table must not be in use by any sequence of the call (pages may be shared
+ * between sequences, so nothing moves in place).  Heads choose apart: position i
+ * may hold different tokens in different heads.
+ * new_lens: device [B], becomes min(lens[b], keep).  kept: device
+ * [B, Hkv, keep], the old positions of the tokens that stayed, -1 behind them.
+ * Neither may be s->lens, nor dst_table be s->table.
+ */
+SAGE_API sage_status sage_kv_evict(const sage_kv_cache *c, const sage_kv_seqs *s, const int32_t *dst_table,
+                                   int32_t dst_pages, int32_t keep, int32_t sinks, int32_t recent,
+                                   int32_t *new_lens, int32_t *kept, void *stream);
+
+typedef struct {
+    int32_t B, Hq, Hkv, N, d;  /* as in sage_params */
+    int32_t dtype;             /* sage_dtype of Q, K, V and O */
+    int32_t layout;            /* sage_layout of q, k, v and o */
+    int32_t window, sinks;     /* window >= 1 (or 0: causal without a window), sinks >= 0 */
+    float   sm_scale;          /* <= 0 selects 1/sqrt(d) */
+} sage_window_params;
+
+/*
+ * Sliding-window attention with sinks over whole sequences (the local layers
+ * of a model), in the inputs' 16-bit type, with fp32 sums and softmax.
+ * q, k, v, o: device, contiguous, in the layout of p.  lse: device fp32
+ * [B, Hq, N] or NULL.  lens: device [B] or NULL (N for every sequence): rows
+ * i >= lens[b] of o and lse are left as they are and of k, v are not used
+ * (values outside [0, N] are taken as the nearest bound).  A key that a row does
+ * not see has no influence on that row, whatever it holds.
+ */
+SAGE_API sage_status sage_attn_window_fwd(const void *q, const void *k, const void *v, void *o, float *lse,
+                                          const int32_t *lens, const sage_window_params *p, void *stream);
 
 /* Human-readable name of a status code (static storage). */
 SAGE_API const char *sage_status_string(sage_status s);

@@ -8,3 +8,7 @@
 #include "peak.cu"
 #include "api.cu"
 #include "noalloc.cu"
+#include "kv_cache.cu"
+#include "decode.cu"
+#include "attn_window.cu"
+#include "api_serving.cu"

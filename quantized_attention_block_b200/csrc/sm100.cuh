@@ -15,6 +15,11 @@ namespace sage {
 __device__ unsigned int g_device_error = 0;
 enum : unsigned int { kDevErrTimeout = 7 };
 
+// A page number or length outside the paged cache since the host last read it
+// (0 = none).  Apart from g_device_error: the prefill kernels refuse to run
+// while that one is set, and a bad page concerns no prefill.
+__device__ unsigned int g_page_error = 0;
+
 // Wait limit in nanoseconds of %globaltimer (default 4 s; a debug entry point
 // shortens it).
 __device__ unsigned long long g_wait_limit_ns = 4000000000ull;

@@ -21,7 +21,7 @@ SAGE_OK = 0
 STATUS_NAMES = {
     0: "SAGE_OK", 1: "SAGE_ERR_INVALID_ARG", 2: "SAGE_ERR_UNSUPPORTED_HEADDIM",
     3: "SAGE_ERR_UNSUPPORTED_DTYPE", 4: "SAGE_ERR_UNSUPPORTED_ARCH", 5: "SAGE_ERR_WORKSPACE_TOO_SMALL",
-    6: "SAGE_ERR_CUDA", 7: "SAGE_ERR_TIMEOUT", 8: "SAGE_ERR_MISALIGNED",
+    6: "SAGE_ERR_CUDA", 7: "SAGE_ERR_TIMEOUT", 8: "SAGE_ERR_MISALIGNED", 9: "SAGE_ERR_BAD_PAGE",
 }
 EXPORTED = ("sage_workspace_bytes", "sage_quant_qkv", "sage_attn_fwd_quantized", "sage_attn_fwd",
             "sage_debug_qk_int32", "sage_last_device_error", "sage_debug_bounded_wait",
@@ -30,7 +30,8 @@ EXPORTED = ("sage_workspace_bytes", "sage_quant_qkv", "sage_attn_fwd_quantized",
             "sage_attn_fwd_nvfp4", "sage_debug_qk_nvfp4", "sage_debug_exp2_poly",
             "sage_debug_kv_quant_two_pass", "sage_quant_kernel_count", "sage_quant_nvfp4_kernel_count",
             "sage_attn_fwd_quantized_lse", "sage_attn_fwd_lse", "sage_debug_mma_rate",
-            "sage_debug_wait_limit")
+            "sage_debug_wait_limit", "sage_kv_append", "sage_decode_workspace_bytes", "sage_attn_decode",
+            "sage_kv_evict", "sage_attn_window_fwd")
 
 
 class SageError(RuntimeError):
@@ -63,6 +64,29 @@ class SageNvfp4View(ctypes.Structure):
                 ("sfq", ctypes.c_void_p), ("sfk", ctypes.c_void_p), ("sfv", ctypes.c_void_p),
                 ("km", ctypes.c_void_p), ("qbar", ctypes.c_void_p), ("dS", ctypes.c_void_p),
                 ("Np", ctypes.c_int64)]
+
+
+class SageKvCache(ctypes.Structure):
+    _fields_ = [("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("quantized", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("weight", ctypes.c_void_p)]
+
+
+class SageKvSeqs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("table", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p)]
+
+
+class SageDecodeParams(ctypes.Structure):
+    _fields_ = [("Hq", ctypes.c_int32), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                ("sm_scale", ctypes.c_float)]
+
+
+class SageWindowParams(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("sm_scale", ctypes.c_float)]
 
 
 _lib = None
@@ -106,6 +130,16 @@ def lib() -> ctypes.CDLL:
         L.sage_quant_kernel_count.restype = ctypes.c_int
         L.sage_quant_nvfp4_kernel_count.argtypes = [P, ctypes.POINTER(ctypes.c_int32)]
         L.sage_quant_nvfp4_kernel_count.restype = ctypes.c_int
+        C, S = ctypes.POINTER(SageKvCache), ctypes.POINTER(SageKvSeqs)
+        D, W = ctypes.POINTER(SageDecodeParams), ctypes.POINTER(SageWindowParams)
+        L.sage_kv_append.argtypes, L.sage_kv_append.restype = [vp, vp, vp, vp, i32, i32, C, S, vp], ctypes.c_int
+        L.sage_decode_workspace_bytes.argtypes = [C, S, D]
+        L.sage_decode_workspace_bytes.restype = ctypes.c_size_t
+        L.sage_attn_decode.argtypes = [vp, vp, vp, vp, C, S, D, vp, ctypes.c_size_t, vp]
+        L.sage_attn_decode.restype = ctypes.c_int
+        L.sage_kv_evict.argtypes = [C, S, vp, i32, i32, i32, i32, vp, vp, vp]
+        L.sage_kv_evict.restype = ctypes.c_int
+        L.sage_attn_window_fwd.argtypes, L.sage_attn_window_fwd.restype = [vp, vp, vp, vp, vp, vp, W, vp], ctypes.c_int
         for n in ("sage_quant_qkv", "sage_attn_fwd_quantized", "sage_attn_fwd", "sage_debug_qk_int32",
                   "sage_last_device_error", "sage_debug_bounded_wait", "sage_quant_nvfp4",
                   "sage_attn_fwd_nvfp4_quantized", "sage_attn_fwd_nvfp4", "sage_debug_qk_nvfp4"):
@@ -387,6 +421,300 @@ def nvfp4_view_tensors(view: SageNvfp4View, p: SageParams, workspace: torch.Tens
         out["qbar"] = sl(view.qbar, 4 * B * Hq * Tm * d, torch.float32, (B, Hq, Tm, d))
         out["dS"] = sl(view.dS, 4 * B * Hq * Tm * Np, torch.float32, (B, Hq, Tm, Np))
     return out
+
+
+# ---------------------------------------------------------------- serving: paged cache, one-token and window attention
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def _expect(name: str, t: torch.Tensor, shape, dtype) -> None:
+    """A contiguous tensor of this shape (None: any extent) and type, else ValueError."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _one_device(**ts) -> torch.device:
+    """The CUDA device that all the tensors (None: absent) are on."""
+    device = None
+    for name, t in ts.items():
+        if t is None:
+            continue
+        device = t.device if device is None else device
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, got {device}")
+    return device
+
+
+def _layout(tensor_layout: str) -> int:
+    if tensor_layout not in LAYOUTS:
+        raise ValueError(f"tensor_layout must be one of {sorted(LAYOUTS)}")
+    return LAYOUTS[tensor_layout]
+
+
+def _range32(**ns) -> None:
+    for name, n in ns.items():
+        if not 0 <= n < 2 ** 31:
+            raise ValueError(f"{name} must be in [0, 2^31), got {n}")
+
+
+def _raw_stream(stream, device) -> int:
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _empty_on(stream, *specs):
+    """Tensors for work on `stream` (None: the current one), made so that the allocator knows it."""
+    if stream is None:
+        return [torch.empty(shape, dtype=dt, device=dev) for shape, dt, dev in specs]
+    with torch.cuda.stream(stream):
+        return [torch.empty(shape, dtype=dt, device=dev) for shape, dt, dev in specs]
+
+
+class KVCache:
+    """A pool of pages of keys and values (sage_kv_cache), around the caller's tensors.
+
+    k_pages, v_pages: [n_pages, Hkv, page_size, d] (tensor_layout "HND") or
+    [n_pages, page_size, Hkv, d] ("NHD"); bf16 or fp16, or int8 keys with
+    float8_e4m3fn values, which need k_scale and v_scale, fp32
+    [n_pages, Hkv, page_size] in either layout.  weight (same shape, optional):
+    the attention weight that each cached token has gathered.  `alloc` makes the
+    tensors.  The pages of a sequence are named by the page table of each call.
+    """
+
+    def __init__(self, k_pages, v_pages, k_scale=None, v_scale=None, weight=None, *, tensor_layout: str = "HND"):
+        layout = _layout(tensor_layout)
+        if k_pages.dim() != 4:
+            raise ValueError(f"k_pages must have 4 dimensions, got {tuple(k_pages.shape)}")
+        self.quantized = k_pages.dtype == torch.int8
+        _expect("k_pages", k_pages, k_pages.shape, k_pages.dtype)
+        _expect("v_pages", v_pages, k_pages.shape, torch.float8_e4m3fn if self.quantized else k_pages.dtype)
+        if not self.quantized and k_pages.dtype not in _DTYPES:
+            raise ValueError(f"pages must be bfloat16, float16 or int8 (keys), got {k_pages.dtype}")
+        n_pages, a, b, d = k_pages.shape
+        heads, page = (a, b) if layout == 0 else (b, a)
+        if page < 16 or page > 1024 or page & (page - 1):
+            raise ValueError(f"page_size must be a power of two from 16 to 1024, got {page}")
+        if d not in (64, 128):
+            raise ValueError(f"head_dim must be 64 or 128, got {d}")
+        if self.quantized != (k_scale is not None) or self.quantized != (v_scale is not None):
+            raise ValueError("k_scale and v_scale go with int8 keys and float8_e4m3fn values")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale), ("weight", weight)):
+            if t is not None:
+                _expect(name, t, (n_pages, heads, page), torch.float32)
+        self.k_pages, self.v_pages, self.k_scale, self.v_scale, self.weight = k_pages, v_pages, k_scale, v_scale, weight
+        self.n_pages, self.Hkv, self.page_size, self.d, self.tensor_layout = n_pages, heads, page, d, tensor_layout
+        self.device = k_pages.device
+        for t in (v_pages, k_scale, v_scale, weight):
+            if t is not None and t.device != self.device:
+                raise ValueError(f"the cache's tensors must be on one device, got {self.device} and {t.device}")
+        # one struct for each type of the tokens (a 16-bit cache has one)
+        self._c = {dt: SageKvCache(heads, d, code, int(self.quantized), page, n_pages, layout, _ptr(k_pages),
+                                   _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(weight))
+                   for dt, code in _DTYPES.items() if self.quantized or dt == k_pages.dtype}
+
+    @classmethod
+    def alloc(cls, n_pages: int, page_size: int, Hkv: int, d: int, dtype=torch.bfloat16, *, quantized: bool = False,
+              track_weight: bool = False, tensor_layout: str = "HND", device="cuda") -> "KVCache":
+        """An empty pool: 16-bit pages of `dtype`, or INT8 keys and E4M3 values."""
+        shape = (n_pages, Hkv, page_size, d) if _layout(tensor_layout) == 0 else (n_pages, page_size, Hkv, d)
+        k = torch.zeros(shape, dtype=torch.int8 if quantized else dtype, device=device)
+        v = torch.zeros(shape, dtype=torch.int8, device=device).view(torch.float8_e4m3fn) if quantized else k.clone()
+        scale = (n_pages, Hkv, page_size)
+        s = [torch.zeros(scale, dtype=torch.float32, device=device) if quantized else None for _ in range(2)]
+        w = torch.zeros(scale, dtype=torch.float32, device=device) if track_weight else None
+        return cls(k, v, *s, w, tensor_layout=tensor_layout)
+
+    def _struct(self, dtype) -> SageKvCache:
+        if dtype not in self._c:
+            raise ValueError(f"the cache takes tokens of {' or '.join(map(str, self._c))}, got {dtype}")
+        return self._c[dtype]
+
+    def _seqs(self, page_table, lens) -> SageKvSeqs:
+        _expect("page_table", page_table, (None, None), torch.int32)
+        B, max_pages = page_table.shape
+        _expect("lens", lens, (B,), torch.int32)
+        if B < 1 or max_pages < 1:
+            raise ValueError(f"page_table must not be empty, got {tuple(page_table.shape)}")
+        return SageKvSeqs(B, max_pages, page_table.data_ptr(), lens.data_ptr())
+
+
+def sage_kv_append(k, v, cache: KVCache, page_table, lens, *, n_new=None, km=None, tensor_layout: str = "HND",
+                   stream=None) -> None:
+    """Write new tokens k, v [B,Hkv,T,d] ("NHD": [B,T,Hkv,d]) behind the lens[b] tokens that sequence
+    b holds in the pages page_table[b] (int32 [B, max_pages]); of sequence b the first n_new[b]
+    (default: T).  lens is not changed.  Quantised caches store INT8 codes of k - km (km: fp32
+    [B,Hkv,d], optional) and E4M3 codes of v, with one scale per token and head."""
+    layout = _layout(tensor_layout)
+    c, s = cache._struct(k.dtype), cache._seqs(page_table, lens)
+    T = k.shape[2 - layout] if k.dim() == 4 else 0
+    shape = (s.B, cache.Hkv, T, cache.d) if layout == 0 else (s.B, T, cache.Hkv, cache.d)
+    _expect("k", k, shape, k.dtype)
+    _expect("v", v, shape, k.dtype)
+    if n_new is not None:
+        _expect("n_new", n_new, (s.B,), torch.int32)
+    if km is not None:
+        if not cache.quantized:
+            raise ValueError("km goes with a quantized cache")
+        _expect("km", km, (s.B, cache.Hkv, cache.d), torch.float32)
+    device = _one_device(k=k, v=v, cache=cache.k_pages, page_table=page_table, lens=lens, n_new=n_new, km=km)
+    with torch.cuda.device(device):
+        _check(lib().sage_kv_append(k.data_ptr(), v.data_ptr(), _ptr(n_new), _ptr(km), T, layout, ctypes.byref(c),
+                                    ctypes.byref(s), _raw_stream(stream, device)), "sage_kv_append")
+
+
+def decode_workspace_bytes(cache: KVCache, page_table, lens, Hq: int, *, window: int = 0, sinks: int = 0) -> int:
+    """Bytes of workspace of sage_attn_decode for these sizes (0: invalid)."""
+    _range32(window=window, sinks=sinks)
+    p = SageDecodeParams(Hq, window, sinks, 0.0)
+    c = next(iter(cache._c.values()))
+    return int(lib().sage_decode_workspace_bytes(ctypes.byref(c), ctypes.byref(cache._seqs(page_table, lens)),
+                                                 ctypes.byref(p)))
+
+
+def _decode(q, cache, page_table, lens, window, sinks, sm_scale, km, out, lse, want_lse, workspace, stream):
+    _range32(window=window, sinks=sinks)
+    c, s = cache._struct(q.dtype), cache._seqs(page_table, lens)
+    _expect("q", q, (s.B, None, cache.d), q.dtype)
+    Hq = q.shape[1]
+    if Hq < 1 or Hq % cache.Hkv:
+        raise ValueError(f"query heads must be a multiple of {cache.Hkv}, got {Hq}")
+    if out is not None:
+        _expect("out", out, q.shape, q.dtype)
+    if lse is not None:
+        _expect("lse", lse, (s.B, Hq), torch.float32)
+    if km is not None:
+        if not cache.quantized:
+            raise ValueError("km goes with a quantized cache")
+        _expect("km", km, (s.B, cache.Hkv, cache.d), torch.float32)
+    if workspace is not None:
+        _expect("workspace", workspace, (None,), torch.uint8)
+    device = _one_device(q=q, cache=cache.k_pages, page_table=page_table, lens=lens, km=km, out=out, lse=lse,
+                         workspace=workspace)
+    p = SageDecodeParams(Hq, window, sinks, float(sm_scale if sm_scale else 0.0))
+    L = lib()
+    with torch.cuda.device(device):
+        if out is None:
+            out, = _empty_on(stream, (q.shape, q.dtype, device))
+        if lse is None and want_lse:
+            lse, = _empty_on(stream, ((s.B, Hq), torch.float32, device))
+        if workspace is None:
+            n = L.sage_decode_workspace_bytes(ctypes.byref(c), ctypes.byref(s), ctypes.byref(p))
+            workspace, = _empty_on(stream, ((n,), torch.uint8, device))
+        _check(L.sage_attn_decode(q.data_ptr(), out.data_ptr(), _ptr(lse), _ptr(km), ctypes.byref(c), ctypes.byref(s),
+                                  ctypes.byref(p), workspace.data_ptr(), workspace.numel(),
+                                  _raw_stream(stream, device)), "sage_attn_decode")
+    return out, lse
+
+
+def sage_attn_decode(q, cache: KVCache, page_table, lens, *, window: int = 0, sinks: int = 0,
+                     sm_scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of one new token a sequence: q [B,Hq,d] at position lens[b] - 1 over the lens[b] tokens
+    of sequence b in the cache -> [B,Hq,d].  window > 0: the last `window` keys and the first `sinks`
+    tokens alone.  If the cache tracks weights, they grow by this token's attention."""
+    return _decode(q, cache, page_table, lens, window, sinks, sm_scale, None, out, None, False, workspace, stream)[0]
+
+
+def sage_attn_decode_lse(q, cache: KVCache, page_table, lens, *, window: int = 0, sinks: int = 0,
+                         sm_scale: Optional[float] = None, km=None, out: Optional[torch.Tensor] = None,
+                         lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """sage_attn_decode that also returns each head's log-sum-exp of the scores (fp32 [B,Hq], natural log;
+    with km, the mean that a quantized cache's keys are stored without, for the keys as they were):
+    (out, lse)."""
+    return _decode(q, cache, page_table, lens, window, sinks, sm_scale, km, out, lse, True, workspace, stream)
+
+
+def sage_kv_evict(cache: KVCache, page_table, lens, dst_table, keep: int, *, sinks: int = 0, recent: int = 0,
+                  new_lens: Optional[torch.Tensor] = None, kept: Optional[torch.Tensor] = None, stream=None):
+    """Hold every sequence to `keep` tokens: the first `sinks`, the last `recent`, and those of the others
+    with the largest gathered weight, per head.  They move, in order, to the pages dst_table [B, n] (int32),
+    which no sequence may be using.  Returns (new_lens [B], kept [B,Hkv,keep]: old positions, -1 behind)."""
+    if cache.weight is None:
+        raise ValueError("the cache does not track weights")
+    _range32(keep=keep, sinks=sinks, recent=recent)
+    if keep < 1 or sinks + recent > keep:
+        raise ValueError(f"keep must be at least 1 and hold sinks and recent, got {keep}, {sinks}, {recent}")
+    c, s = next(iter(cache._c.values())), cache._seqs(page_table, lens)
+    _expect("dst_table", dst_table, (s.B, None), torch.int32)
+    if dst_table.shape[1] * cache.page_size < keep:
+        raise ValueError(f"dst_table holds {dst_table.shape[1]} pages of {cache.page_size}: too few for {keep} tokens")
+    if new_lens is not None:
+        _expect("new_lens", new_lens, (s.B,), torch.int32)
+    if kept is not None:
+        _expect("kept", kept, (s.B, cache.Hkv, keep), torch.int32)
+    device = _one_device(cache=cache.k_pages, page_table=page_table, lens=lens, dst_table=dst_table,
+                         new_lens=new_lens, kept=kept)
+    with torch.cuda.device(device):
+        if new_lens is None:
+            new_lens, = _empty_on(stream, ((s.B,), torch.int32, device))
+        if kept is None:
+            kept, = _empty_on(stream, ((s.B, cache.Hkv, keep), torch.int32, device))
+        _check(lib().sage_kv_evict(ctypes.byref(c), ctypes.byref(s), dst_table.data_ptr(), dst_table.shape[1], keep,
+                                   sinks, recent, new_lens.data_ptr(), kept.data_ptr(),
+                                   _raw_stream(stream, device)), "sage_kv_evict")
+    return new_lens, kept
+
+
+def _window_fwd(q, k, v, window, sinks, lens, sm_scale, out, lse, want_lse, stream, tensor_layout):
+    layout = _layout(tensor_layout)
+    _range32(window=window, sinks=sinks)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError(f"q and k must have 4 dimensions, got {tuple(q.shape)} and {tuple(k.shape)}")
+    if q.dtype not in _DTYPES:
+        raise ValueError(f"q must be bfloat16 or float16, got {q.dtype}")
+    B, Hq, N, d = q.shape if layout == 0 else (q.shape[0], q.shape[2], q.shape[1], q.shape[3])
+    Hkv = k.shape[1 + layout]
+    kv_shape = (B, Hkv, N, d) if layout == 0 else (B, N, Hkv, d)
+    _expect("q", q, q.shape, q.dtype)
+    _expect("k", k, kv_shape, q.dtype)
+    _expect("v", v, kv_shape, q.dtype)
+    if lens is not None:
+        _expect("lens", lens, (B,), torch.int32)
+    if out is not None:
+        _expect("out", out, q.shape, q.dtype)
+    if lse is not None:
+        _expect("lse", lse, (B, Hq, N), torch.float32)
+    device = _one_device(q=q, k=k, v=v, lens=lens, out=out, lse=lse)
+    p = SageWindowParams(B, Hq, Hkv, N, d, _DTYPES[q.dtype], layout, window, sinks, float(sm_scale if sm_scale else 0.0))
+    with torch.cuda.device(device):
+        made = []
+        if out is None:
+            out, = _empty_on(stream, (q.shape, q.dtype, device))
+            made.append(out)
+        if lse is None and want_lse:
+            lse, = _empty_on(stream, ((B, Hq, N), torch.float32, device))
+            made.append(lse)
+        raw = _raw_stream(stream, device)
+        if lens is not None:  # rows behind a sequence's end are not written: zeros in tensors made here
+            with torch.cuda.stream(stream):
+                for t in made:
+                    t.zero_()
+        _check(lib().sage_attn_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse),
+                                          _ptr(lens), ctypes.byref(p), raw), "sage_attn_window_fwd")
+    return out, lse
+
+
+def sage_attn_window_fwd(q, k, v, *, window: int, sinks: int = 0, lens=None, sm_scale: Optional[float] = None,
+                         out: Optional[torch.Tensor] = None, stream=None, tensor_layout: str = "HND") -> torch.Tensor:
+    """Sliding-window causal attention in the inputs' 16-bit type: row i sees the last `window` keys up to
+    its own (0: all of them) and the first `sinks`.  [B,Hq,N,d] x [B,Hkv,N,d] -> [B,Hq,N,d] ("NHD":
+    [B,N,H,d]).  lens (int32 [B], optional): rows behind a sequence's length are not written (zeros in an
+    output made here) and not read."""
+    return _window_fwd(q, k, v, window, sinks, lens, sm_scale, out, None, False, stream, tensor_layout)[0]
+
+
+def sage_attn_window_fwd_lse(q, k, v, *, window: int, sinks: int = 0, lens=None, sm_scale: Optional[float] = None,
+                             out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, stream=None,
+                             tensor_layout: str = "HND"):
+    """sage_attn_window_fwd that also returns each row's log-sum-exp (fp32 [B,Hq,N], natural log): (out, lse)."""
+    return _window_fwd(q, k, v, window, sinks, lens, sm_scale, out, lse, True, stream, tensor_layout)
 
 
 def attention_ops(B: int, Hq: int, N: int, d: int, causal: bool) -> float:
