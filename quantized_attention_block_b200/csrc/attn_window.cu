@@ -9,16 +9,26 @@
 // needs no rescaling, and m cancels in o and lse whatever it is.
 //
 // A work item is 256 query rows of one head: two tiles of 128 rows that share
-// every 128-key tile of K and V.  One CTA an SM takes items in turn (persistent:
-// the next item's loads and first products run under the last one's softmax and
-// output).  512 threads in four warpgroups:
+// every 128-key tile of K and V.  One CTA an SM takes items in turn (the next
+// item's loads and first products run under the last one's softmax and output);
+// which, it learns from the hardware's launch queue (clc_try_cancel: the grid has
+// a CTA an item, and a running one takes the place of one that has not started).
+// 512 threads in four warpgroups:
 //   WG0, 1  softmax of row tile 0 and 1 (thread = row = TMEM lane)
 //   WG2     output of both tiles
-//   WG3     warp 0: TMA producer; warp 1: MMA issuer (one thread) and TMEM owner
-// TMEM (512 columns): S_i at 128 i; P_i (16 bit) over the upper half of S_i, as
-// the A operand of P V; O_i at 256 + D i.  A row tile's chain is
-// S(0) P V(0) S(1) ...; the two tiles' chains keep the tensor core busy while
-// the other tile's softmax runs.
+//   WG3     warp 0: TMA producer; warps 1, 2: MMA issuers of row tile 0 and 1 (one
+//           thread each); warp 3: takes the items
+// A step of a row tile is 64 keys: S = Q K^T, softmax, O += P V.  TMEM (512
+// columns): two buffers of S a row tile, at 128 i + 64 b, with P (16 bit, the A
+// operand of P V) over the first half of its S; O_i at 256 + D i.  S of the next
+// step is computed while the softmax works on this one, so a row's chain never
+// waits for the tensor core.  (Steps of 128 keys, whose S fills the columns that
+// both buffers have here, left the softmax waiting 1400 of 4000 cycles for
+// P V and the next S; N = 64 costs the Q K^T half of its rate instead, since A
+// and B then take 6 KB of shared memory for 32 cycles of products.)
+// Each row tile has an issuing warp of its own: one thread that polled for both
+// spent longer on its bookkeeping (some 2500 cycles for 128 keys) than the tensor
+// core on the products.
 //
 // Keys a row does not see are -inf before the maximum, so their weights are
 // exact zeros; a NaN or infinity in such a key's V still makes 0 x inf = NaN in
@@ -26,6 +36,7 @@
 // visible keys alone (window_row).  Rows of V behind a sequence's end (padding,
 // which may hold anything) are zeroed in shared memory first.
 #include <climits>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -38,20 +49,20 @@ namespace sage {
 namespace {
 
 constexpr int kWinThreads = 512;
-constexpr int kNarrow = 32;            // rows of the narrow key tile (few sinks)
+constexpr int kStep = 64;              // keys of a step; rows of a half key tile (few sinks)
+// Of every 16 pairs of weights in a tile without masked keys, those whose bit is set take 2^x
+// on the FMA pipe: the MUFU's 16 a clock and SM alone would take as long as both products.
+constexpr unsigned kWinPoly = 0x8888;
 constexpr float kWinSlack = 8.0f;      // log2 of the largest weight before O is rescaled
-// registers a thread of the softmax, output and producer / MMA warpgroups
-constexpr uint32_t kWinRegsSoftmax = 192, kWinRegsOut = 80, kWinRegsIssue = 48;
-static_assert(2 * kWinRegsSoftmax + kWinRegsOut + kWinRegsIssue <= 512, "register split exceeds the launch");
-
 template <int D>
 struct WinSmem {
   static constexpr uint32_t kTileBytes = 128 * D * 2;
   static constexpr int kRing = D == 128 ? 5 : 8;  // K and V tiles in turn
   static constexpr uint32_t oRing = 2 * kTileBytes;
   static constexpr uint32_t oL = oRing + kRing * kTileBytes;  // float2[2][128]: l, sm_scale log2(e) m
-  static constexpr uint32_t oBar = oL + 2 * 128 * 8;
-  static constexpr uint32_t kBars = 2 * kRing + 1 + 2 * 9 + 1;
+  static constexpr uint32_t oItem = oL + 2 * 128 * 8;         // WinItem[2], then the launch queue's answer
+  static constexpr uint32_t oBar = oItem + 2 * 32 + 16;
+  static constexpr uint32_t kBars = 2 * kRing + 1 + 2 * 13;
   static constexpr uint32_t oTmem = oBar + 8 * kBars;
   static constexpr uint32_t kBytes = oTmem + 16;
   static_assert(kBytes <= 227 * 1024, "window attention buffers exceed the shared memory of one CTA");
@@ -59,46 +70,61 @@ struct WinSmem {
 
 // The key tiles of a work item: sink tiles [0, ns) with keys 128 j.., then the
 // tiles of the window, keys 128 (t0 + j - ns)..  Row tile i takes the sink tiles
-// and [lo[i], hi[i]].
-struct WinItem {
+// and [lo(i), hi(i)], in steps of 64 keys.
+struct __align__(16) WinItem {
   int b, h, q0, n;
-  int ns, t0, nt;
-  int lo[2], hi[2];
-  __device__ __forceinline__ int count(int i) const { return hi[i] < lo[i] ? 0 : ns + hi[i] - lo[i] + 1; }
-  __device__ __forceinline__ int tile(int i, int k) const { return k < ns ? k : lo[i] + k - ns; }
+  int ns, t0, nt;  // nt: key tiles of the item; 0: no more items
+  int window;
+  __device__ __forceinline__ int lead(int i) const { return q0 + 128 * i - window + 1; }  // first key of the window
+  __device__ __forceinline__ int lo(int i) const { return ns + (t0 > 0 && lead(i) > 0 ? lead(i) / 128 : 0) - t0; }
+  __device__ __forceinline__ int hi(int i) const { return ns + q0 / 128 + i - t0; }
+  __device__ __forceinline__ bool rows(int i) const { return q0 + 128 * i < n; }
   __device__ __forceinline__ int key0(int j) const { return 128 * (j < ns ? j : t0 + j - ns); }
 };
+// A walk over the steps of row tile i (j == nt: past the last).  Steps whose keys no row sees are left out.
+struct WinWalk {
+  int i, lo, hi, j, sub, end;  // the step's key tile and half; halves of the tile
+  __device__ __forceinline__ void enter(const WindowArgs& a, const WinItem& w, int t) {
+    if (t >= w.ns && t < lo) t = lo;
+    j = t > hi ? w.nt : t;
+    const int key0 = w.key0(j);
+    end = (j < w.ns ? a.sinks : w.n) - key0 <= kStep ? 1 : 2;
+    sub = j == lo && w.t0 > 0 && w.lead(i) - key0 >= kStep ? 1 : 0;
+  }
+  __device__ __forceinline__ void begin(const WindowArgs& a, const WinItem& w, int tile) {
+    i = tile;
+    lo = w.lo(i);
+    hi = w.hi(i);
+    if (w.rows(i)) enter(a, w, 0);
+    else j = w.nt;
+  }
+  __device__ __forceinline__ void next(const WindowArgs& a, const WinItem& w) {
+    if (++sub >= end) enter(a, w, j + 1);
+  }
+};
+static_assert(sizeof(WinItem) == 32, "items are passed through shared memory as two 16-byte words");
 
-__device__ __forceinline__ WinItem win_item(const WindowArgs& a, int idx) {
+__device__ __forceinline__ WinItem win_item(const WindowArgs& a, uint32_t idx) {
   // heads in groups whose K and V stay in L2 while every pair of their rows runs, heaviest rows first
   WinItem w;
-  const int pairs = (a.N + 255) / 256, per = a.group * pairs;
-  const int g = idx / per, in = idx % per;
-  const int heads = min(a.group, a.B * a.Hq - g * a.group);
-  const int bh = g * a.group + in % heads;
+  const uint32_t per = a.group * a.pairs, g = idx / per, in = idx - g * per;
+  const uint32_t heads = min((uint32_t)a.group, (uint32_t)(a.B * a.Hq) - g * a.group);
+  const uint32_t pair = in / heads, bh = g * a.group + in - pair * heads;
   w.b = bh / a.Hq;
-  w.h = bh % a.Hq;
-  w.q0 = 256 * (pairs - 1 - in / heads);
+  w.h = bh - w.b * a.Hq;
+  w.q0 = 256 * (a.pairs - 1 - (int)pair);
   w.n = a.lens ? min(max(__ldg(a.lens + w.b), 0), a.N) : a.N;
-  int first[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int lead = w.q0 + 128 * i - a.window + 1;
-    first[i] = a.window > 0 && lead > 0 ? lead / 128 : 0;
-  }
-  if (a.sinks > 128 * first[0]) first[0] = first[1] = 0;  // the sinks reach into the window's tiles
-  w.t0 = first[0];
+  w.window = a.window;
+  const int lead = w.q0 - a.window + 1;
+  w.t0 = a.window > 0 && lead > 0 ? lead / 128 : 0;
+  if (a.sinks > 128 * w.t0) w.t0 = 0;  // the sinks reach into the window's tiles: every tile from 0 on
   w.ns = w.t0 > 0 ? (a.sinks + 127) / 128 : 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    w.lo[i] = w.ns + first[i] - w.t0;
-    w.hi[i] = w.q0 + 128 * i < w.n ? w.ns + w.q0 / 128 + i - w.t0 : w.lo[i] - 1;
-  }
-  w.nt = w.count(0) == 0 ? 0 : max(w.hi[0], w.hi[1]) + 1;
+  w.nt = w.q0 >= w.n ? 0 : w.hi(w.q0 + 128 < w.n ? 1 : 0) + 1;
   return w;
 }
+// the last sink tile is loaded by half if that holds the sinks
 __device__ __forceinline__ bool win_narrow(const WindowArgs& a, const WinItem& w, int j) {
-  return j == w.ns - 1 && a.sinks - 128 * j <= kNarrow;
+  return j == w.ns - 1 && a.sinks - 128 * j <= kStep;
 }
 
 // One row by one warp, over its visible keys alone: lane = key for the scores,
@@ -200,18 +226,36 @@ __device__ __forceinline__ void store_row32(void* p, const uint32_t* w, bool wid
 
 struct WinBars {
   uint64_t* kv_full;   // [ring]
-  uint64_t* kv_empty;  // [ring]  both row tiles' products that read the slot retired
+  uint64_t* kv_empty;  // [ring]  the products of a row tile that read the slot retired (one arrival a row tile)
   uint64_t* part;      // a tile of V that ends behind the sequence landed (its producer zeroes those rows)
   uint64_t* q_full;    // [2]
   uint64_t* q_empty;   // [2]  the item's last Q K^T of tile i retired
-  uint64_t* s_full;    // [2]  Q K^T of tile i retired
-  uint64_t* p_full;    // [2]  P_i written (one arrival a warp)
-  uint64_t* o_done;    // [2]  a P V of tile i retired
+  uint64_t* s_full;    // [tile][buffer]  Q K^T retired
+  uint64_t* p_full;    // [tile][buffer]  P written (one arrival a warp)
+  uint64_t* pv_done;   // [2]  a P V of tile i retired
   uint64_t* o_full;    // [2]  the item's last P V of tile i retired
   uint64_t* o_free;    // [2]  the item's O_i, l and m have been read (one arrival a warp)
   uint64_t* l_ready;   // [2]  l and m of tile i in shared memory (one arrival a warp)
-  uint64_t* mma_done;  // all tensor-core work of the CTA retired
+  uint64_t* mma_done;  // [2]  all tensor-core work of tile i retired
+  uint64_t* item_full;   // [2]  an item is posted
+  uint64_t* item_empty;  // [2]  every warp but the one that takes the items has read it
+  uint64_t* item_want;   // the producer is about to finish the item
+  uint64_t* answer;      // the launch queue answered
 };
+constexpr int kItemReaders = 15;
+
+// The next item, from the ring that the taking warp fills: false without one (w.nt == 0) or if the wait gave up
+__device__ __forceinline__ bool win_next(const WinItem* ring, const WinBars& bar, uint32_t nth, WinItem& w) {
+  const uint32_t s = nth & 1;
+  if (!mbar_wait_warp(&bar.item_full[s], (nth >> 1) & 1)) return false;
+  const uint4* p = reinterpret_cast<const uint4*>(ring + s);
+  const uint4 x = p[0], y = p[1];
+  w.b = x.x, w.h = x.y, w.q0 = x.z, w.n = x.w;
+  w.ns = y.x, w.t0 = y.y, w.nt = y.z, w.window = y.w;
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&bar.item_empty[s]);
+  return w.nt > 0;
+}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kWinThreads, 1)
@@ -222,14 +266,15 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   constexpr int R = L::kRing;
   constexpr uint32_t kF16 = std::is_same<T, __half>::value ? 0u : 1u;  // operand format: fp16 or bf16
   constexpr uint32_t kTransB = 1u << 16;                               // B with its N dimension contiguous
-  constexpr uint32_t kIdescQK = make_idesc(1, kF16, kF16, 128, 128), kIdescQKn = make_idesc(1, kF16, kF16, 128, kNarrow);
+  constexpr uint32_t kIdescQK = make_idesc(1, kF16, kF16, 128, kStep);
   constexpr uint32_t kIdescPV = make_idesc(1, kF16, kF16, 128, D) | kTransB;
-  constexpr uint32_t kTmemCols = 512, kP = 64;  // kP: P_i's first column in S_i
+  constexpr uint32_t kTmemCols = 512;
 
   extern __shared__ __align__(1024) uint8_t smem_win[];
   uint8_t* sQ = smem_win;
   uint8_t* ring = smem_win + L::oRing;
   float2* s_l = reinterpret_cast<float2*>(smem_win + L::oL);
+  WinItem* items = reinterpret_cast<WinItem*>(smem_win + L::oItem);
   WinBars bar;
   bar.kv_full = reinterpret_cast<uint64_t*>(smem_win + L::oBar);
   bar.kv_empty = bar.kv_full + R;
@@ -237,32 +282,42 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   bar.q_full = bar.part + 1;
   bar.q_empty = bar.q_full + 2;
   bar.s_full = bar.q_empty + 2;
-  bar.p_full = bar.s_full + 2;
-  bar.o_done = bar.p_full + 2;
-  bar.o_full = bar.o_done + 2;
+  bar.p_full = bar.s_full + 4;
+  bar.pv_done = bar.p_full + 4;
+  bar.o_full = bar.pv_done + 2;
   bar.o_free = bar.o_full + 2;
   bar.l_ready = bar.o_free + 2;
   bar.mma_done = bar.l_ready + 2;
+  bar.item_full = bar.mma_done + 2;
+  bar.item_empty = bar.item_full + 2;
+  bar.item_want = bar.item_empty + 2;
+  bar.answer = bar.item_want + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_win + L::oTmem);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, wg = warp / 4;
   if (threadIdx.x == 0) {
     for (int s = 0; s < R; ++s) {
       mbar_init(&bar.kv_full[s], 1);
-      mbar_init(&bar.kv_empty[s], 1);
+      mbar_init(&bar.kv_empty[s], 2);
     }
     mbar_init(bar.part, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.q_full[i], 1);
       mbar_init(&bar.q_empty[i], 1);
-      mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i], 4);
-      mbar_init(&bar.o_done[i], 1);
+      mbar_init(&bar.pv_done[i], 1);
       mbar_init(&bar.o_full[i], 1);
       mbar_init(&bar.o_free[i], 4);
       mbar_init(&bar.l_ready[i], 4);
+      mbar_init(&bar.mma_done[i], 1);
+      mbar_init(&bar.item_full[i], 1);
+      mbar_init(&bar.item_empty[i], kItemReaders);
     }
-    mbar_init(bar.mma_done, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_full[i], 4);
+    }
+    mbar_init(bar.item_want, 1);
+    mbar_init(bar.answer, 1);
     mbar_fence_init();
   }
   if (warp == 13) {
@@ -275,7 +330,6 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (wg == 3) {
-    regs_dec<kWinRegsIssue>();
     if (warp == 12) {
       // ------------------------------------------------------------ TMA producer
       if (lane == 0) {
@@ -287,13 +341,14 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       uint32_t idx = 0, parts = 0;  // ring slots filled, partial tiles of V
       uint32_t nq[2] = {0, 0};      // items of tile i
       const int G = a.Hq / a.Hkv;
-      for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
-        const WinItem w = win_item(a, it);
+      WinItem w;
+      for (uint32_t nth = 0; ok && win_next(items, bar, nth, w); ++nth) {
         const int hk = w.h / G;
         for (int j = 0; j < w.nt && ok; ++j) {
+          if (lane == 0 && j == max(0, w.nt - 4)) mbar_arrive(bar.item_want);
           const bool narrow = win_narrow(a, w, j);
           const int key0 = w.key0(j);
-          const uint32_t rows = narrow ? kNarrow : 128, bytes = rows * D * 2, half = rows * 128;
+          const uint32_t rows = narrow ? kStep : 128, bytes = rows * D * 2, half = rows * 128;
           for (int x = 0; x < 2 && ok; ++x, ++idx) {  // K, then V
             const uint32_t s = idx % R;
             // rows of V from here on belong to no token of this sequence (TMA zeroes those behind N itself)
@@ -322,7 +377,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
             if (j == 0 && x == 0 && ok && lane == 0) {
               // Q after the first K: it waits for the last item's last product
               for (int i = 0; i < 2; ++i) {
-                if (w.count(i) == 0) continue;
+                if (!w.rows(i)) continue;
                 if (nq[i] > 0 && !(ok = mbar_wait(&bar.q_empty[i], (nq[i] - 1) & 1))) break;
                 mbar_expect_tx(&bar.q_full[i], L::kTileBytes);
                 for (int c = 0; c < D / 64; ++c)
@@ -341,244 +396,244 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         for (int i = 0; i < 2; ++i)
           if (nq[i] > 0) mbar_wait(&bar.q_full[i], (nq[i] - 1) & 1);
       }
-    } else if (warp == 13) {
-      // ------------------------------------------------------------ MMA issuer
-      if (lane == 0) {
-        // One chain a row tile: S(0), P V(0), S(1), ..., item after item; each step is
-        // issued as soon as its operands are there (non-blocking polls).
-        struct {
-          WinItem w;
-          int it;         // item
-          int k;          // step within the item
-          int g;          // key tiles of the items before this one
-          uint32_t step;  // steps so far (all items)
-          uint32_t items; // items before this one
-          bool pv;        // the step's S is issued, its P V is not
-          bool live;
-        } c[2];
-        auto next_item = [&](auto& ch, int i) {  // the next item that has rows in tile i
-          while (ch.it < a.items) {
-            ch.w = win_item(a, ch.it);
-            if (ch.w.count(i) > 0) break;
-            ch.g += ch.w.nt;
-            ch.it += gridDim.x;
+    } else if (warp < 15) {
+      // ------------------------------------------------------------ MMA issuer of row tile i
+      const int i = warp - 13;
+      const uint32_t tS = tmem + 128 * i, tO = tmem + 256 + D * i;
+      const uint32_t q = smem_u32(sQ + i * L::kTileBytes);
+      const bool one = elect_one();
+      uint32_t g0 = 0, n_items = 0;      // key tiles of the items before; items of this row tile
+      uint32_t s_qk = 0, s_pv = 0;       // steps issued
+      bool ok = true;
+      WinItem w;
+      for (uint32_t nth = 0; ok && win_next(items, bar, nth, w); ++nth) {
+        // the slots of K (x = 0) or V (1) of key tiles [from, to), which this row tile does not see, released unread
+        auto pass = [&](int from, int to, uint32_t x) {
+          for (int j = from; j < to && ok; ++j) {
+            const uint32_t at = 2 * (g0 + j) + x;
+            ok = mbar_wait_warp(&bar.kv_full[at % R], (at / R) & 1);
+            if (ok && lane == 0) mbar_arrive(&bar.kv_empty[at % R]);
           }
-          ch.live = ch.it < a.items;
         };
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          c[i].it = blockIdx.x;
-          c[i].k = c[i].g = 0;
-          c[i].step = c[i].items = 0;
-          c[i].pv = false;
-          next_item(c[i], i);
-        }
-        int rel_k = 0, rel_v = 0;  // key tiles whose K, V slots are released
-        bool ok = true;
-        uint64_t t_idle = 0;
-        while (ok && (c[0].live || c[1].live)) {
-          bool progress = false;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            auto& ch = c[i];
-            if (!ch.live) continue;
-            const int j = ch.w.tile(i, ch.k);
-            const uint32_t g = ch.g + j;
-            const bool narrow = win_narrow(a, ch.w, j);
-            if (!ch.pv) {
-              const uint32_t s = (2 * g) % R;
-              if ((ch.k > 0 || mbar_test_wait(smem_u32(&bar.q_full[i]), ch.items & 1)) &&
-                  mbar_test_wait(smem_u32(&bar.kv_full[s]), (2 * g / R) & 1)) {
-                tc_fence_after();
-                const uint32_t q = smem_u32(sQ + i * L::kTileBytes), k = smem_u32(ring + s * L::kTileBytes);
-                const uint32_t khalf = (narrow ? kNarrow : 128) * 128;
+        WinWalk c, d;  // the next S, the next P V
+        c.begin(a, w, i);
+        d = c;
+        pass(0, c.j, 0);
+        pass(0, d.j, 1);
+        if (w.rows(i)) {
+          ok = ok && mbar_wait_warp(&bar.q_full[i], n_items & 1);
+          bool first = true;
+          while (d.j < w.nt && ok) {
+            // S runs up to two steps ahead: its buffer was that of the P V before the last
+            while (c.j < w.nt && ok && s_qk < s_pv + 2) {
+              const uint32_t at = 2 * (g0 + c.j), slot = at % R;
+              if (!(ok = mbar_wait_warp(&bar.kv_full[slot], (at / R) & 1))) break;
+              tc_fence_after();
+              const int j = c.j, sub = c.sub;
+              const uint32_t half = (win_narrow(a, w, j) ? kStep : 128) * 128;  // bytes of 64 channels of the slot
+              c.next(a, w);
+              if (one) {
+                const uint32_t kt = smem_u32(ring + slot * L::kTileBytes) + sub * kStep * 128;
+                const uint32_t dst = tS + 64 * (s_qk & 1);
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x)
-                  mma_f16(tmem + 128 * i, make_sdesc(q + (x / 4) * 16384 + (x % 4) * 32, 1024, kSwizzle128B),
-                          make_sdesc(k + (x / 4) * khalf + (x % 4) * 32, 1024, kSwizzle128B),
-                          narrow ? kIdescQKn : kIdescQK, x > 0);
-                mma_commit(&bar.s_full[i]);
-                if (ch.k + 1 == ch.w.count(i)) mma_commit(&bar.q_empty[i]);
-                ch.pv = true;
-                progress = true;
+                  mma_f16(dst, make_sdesc(q + (x / 4) * 16384 + (x % 4) * 32, 1024, kSwizzle128B),
+                          make_sdesc(kt + (x / 4) * half + (x % 4) * 32, 1024, kSwizzle128B), kIdescQK, x > 0);
+                mma_commit(&bar.s_full[2 * i + (s_qk & 1)]);
+                if (c.j != j) mma_commit(&bar.kv_empty[slot]);
+                if (c.j == w.nt) mma_commit(&bar.q_empty[i]);
               }
-            } else {
-              const uint32_t s = (2 * g + 1) % R;
-              if (mbar_test_wait(smem_u32(&bar.p_full[i]), ch.step & 1) &&
-                  mbar_test_wait(smem_u32(&bar.kv_full[s]), ((2 * g + 1) / R) & 1) &&
-                  (ch.k > 0 || ch.items == 0 || mbar_test_wait(smem_u32(&bar.o_free[i]), (ch.items - 1) & 1))) {
-                tc_fence_after();
-                const uint32_t v = smem_u32(ring + s * L::kTileBytes), vhalf = (narrow ? kNarrow : 128) * 128;
-                const int nk = narrow ? kNarrow / 16 : 8;
-                for (int x = 0; x < nk; ++x)  // 16 keys: 8 columns of P, 16 rows of V
-                  mma_f16_ts(tmem + 256 + D * i, tmem + 128 * i + kP + 8 * x,
-                             make_sdesc_mn(v + x * 2048, vhalf, 1024, kSwizzle128B), kIdescPV, ch.k > 0 || x > 0);
-                mma_commit(&bar.o_done[i]);
-                ch.pv = false;
-                ++ch.step;
-                if (++ch.k == ch.w.count(i)) {
-                  mma_commit(&bar.o_full[i]);
-                  ch.g += ch.w.nt;
-                  ch.it += gridDim.x;
-                  ch.k = 0;
-                  ++ch.items;
-                  next_item(ch, i);
-                }
-                progress = true;
-              }
+              __syncwarp();
+              ++s_qk;
+              if (c.j > j + 1) pass(j + 1, c.j, 0);
             }
-          }
-          if (progress) {
-            // slots that neither chain will read again
-            int need_k = INT_MAX, need_v = INT_MAX;
+            if (!ok) break;
+            // O += P V: 16 keys are 8 columns of P and 16 rows of V
+            const uint32_t at = 2 * (g0 + d.j) + 1, slot = at % R;
+            if (!(ok = mbar_wait_warp(&bar.kv_full[slot], (at / R) & 1))) break;
+            if (first && n_items > 0 && !(ok = mbar_wait_warp(&bar.o_free[i], (n_items - 1) & 1))) break;
+            if (!(ok = mbar_wait_warp(&bar.p_full[2 * i + (s_pv & 1)], (s_pv >> 1) & 1))) break;
+            tc_fence_after();
+            const int j = d.j, sub = d.sub;
+            const uint32_t half = (win_narrow(a, w, j) ? kStep : 128) * 128;
+            d.next(a, w);
+            if (one) {
+              const uint32_t vt = smem_u32(ring + slot * L::kTileBytes) + sub * kStep * 128;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if (c[i].live) {
-                const int at = c[i].g + c[i].w.tile(i, c[i].k);
-                need_v = min(need_v, at);
-                const int nxt = !c[i].pv ? at
-                                : c[i].k + 1 < c[i].w.count(i) ? c[i].g + c[i].w.tile(i, c[i].k + 1)
-                                                               : c[i].g + c[i].w.nt;
-                need_k = min(need_k, nxt);
-              }
-            if (c[0].live || c[1].live) {
-              for (; rel_k < need_k; ++rel_k) mma_commit(&bar.kv_empty[(2 * rel_k) % R]);
-              for (; rel_v < need_v; ++rel_v) mma_commit(&bar.kv_empty[(2 * rel_v + 1) % R]);
+              for (int x = 0; x < kStep / 16; ++x)
+                mma_f16_ts(tO, tS + 64 * (s_pv & 1) + 8 * x, make_sdesc_mn(vt + x * 2048, half, 1024, kSwizzle128B),
+                           kIdescPV, !first || x > 0);
+              mma_commit(&bar.pv_done[i]);
+              if (d.j != j) mma_commit(&bar.kv_empty[slot]);
+              if (d.j == w.nt) mma_commit(&bar.o_full[i]);
             }
-            t_idle = 0;
-          } else if (t_idle == 0) {
-            t_idle = globaltimer_ns();
-          } else if (globaltimer_ns() - t_idle > g_wait_limit_ns) {
-            record_error(kDevErrTimeout);
-            ok = false;
+            __syncwarp();
+            ++s_pv;
+            first = false;
+            if (d.j > j + 1) pass(j + 1, d.j, 1);
           }
+          ++n_items;
         }
-        // every tensor-core op retired before TMEM is released
-        mma_commit(bar.mma_done);
-        mbar_wait(bar.mma_done, 0);
+        g0 += w.nt;
+      }
+      // every tensor-core op retired before TMEM is released
+      if (one) {
+        mma_commit(&bar.mma_done[i]);
+        mbar_wait(&bar.mma_done[i], 0);
       }
       __syncwarp();
+    } else {
+      // ------------------------------------------------------------ takes the items
+      uint32_t idx = blockIdx.x, asked = 0;
+      bool have = true;  // idx is an item
+      auto ask = [&] {
+        bool got = false;
+        if (lane == 0) {
+          mbar_expect_tx(bar.answer, 16);
+          clc_try_cancel(items + 2, bar.answer);
+          got = mbar_wait(bar.answer, asked & 1) && clc_answer(items + 2, idx);
+          fence_proxy_async_smem();  // the answer is read before the next one may land
+        }
+        ++asked;
+        have = __shfl_sync(0xffffffffu, (int)got, 0);
+        idx = __shfl_sync(0xffffffffu, idx, 0);
+      };
+      for (uint32_t nth = 0;; ++nth) {
+        WinItem w;
+        w.nt = 0;
+        while (have) {
+          w = win_item(a, idx);
+          if (w.nt > 0) break;
+          ask();  // (an item without rows is passed over)
+        }
+        if (nth >= 2 && !mbar_wait_warp(&bar.item_empty[nth & 1], ((nth >> 1) - 1) & 1)) break;
+        if (lane == 0) {
+          items[nth & 1] = w;
+          mbar_arrive(&bar.item_full[nth & 1]);
+        }
+        if (w.nt == 0) break;
+        // not before the item is nearly done: an item taken early is one that an idle CTA cannot take
+        if (!mbar_wait_warp(bar.item_want, nth & 1)) break;
+        ask();
+      }
     }
   } else if (wg < 2) {
     // ------------------------------------------------------------ softmax
-    regs_inc<kWinRegsSoftmax>();
     const int ti = wg, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    const uint32_t tS = tmem + 128 * ti + lanes, tO = tmem + 256 + D * ti + lanes;
+    const uint32_t tO = tmem + 256 + D * ti + lanes;
     const float scale = a.scale_log2, slack = kWinSlack / scale;
-    uint32_t step = 0, items = 0;
+    uint32_t step = 0, n_items = 0;
     bool ok = true;
-    for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
-      const WinItem w = win_item(a, it);
-      const int count = w.count(ti);
-      if (count == 0) continue;
+    WinItem w;
+    for (uint32_t nth = 0; ok && win_next(items, bar, nth, w); ++nth) {
+      if (!w.rows(ti)) continue;
       const int p0 = w.q0 + 128 * ti, p = p0 + row;
       float m = -INFINITY, l = 0.0f;
-      for (int k = 0; k < count && ok; ++k, ++step) {
-        const int j = w.tile(ti, k), key0 = w.key0(j);
-        const int hi = p - key0, lo = a.window > 0 ? hi - a.window + 1 : INT_MIN, sk = a.sinks - key0;
-        // columns c <= hi and (c >= lo or c < sk) are visible
-        const bool masked = key0 + 127 > p0 || (a.window > 0 && p0 + 128 - a.window > key0 && sk < 128);
-        const bool narrow = win_narrow(a, w, j);
-        if (!(ok = mbar_wait_warp(&bar.s_full[ti], step & 1))) break;
+      WinWalk c;
+      c.begin(a, w, ti);
+      for (; c.j < w.nt; ++step) {
+        const uint32_t tS = tmem + 128 * ti + 64 * (step & 1) + lanes;
+        const int key0 = w.key0(c.j) + kStep * c.sub;
+        const int end = c.j < w.ns ? a.sinks - key0 : INT_MAX;  // columns of a sink tile that are sinks
+        const bool masked = end < kStep || key0 + kStep - 1 > p0 ||
+                            (a.window > 0 && c.j >= w.ns && p0 + 128 - a.window > key0 && a.sinks - key0 < kStep);
+        if (!(ok = mbar_wait_warp(&bar.s_full[2 * ti + (step & 1)], (step >> 1) & 1))) break;
         tc_fence_after();
-        uint32_t s[128];
+        uint32_t s[kStep];
         tmem_ld32p(tS, s);
-        if (!narrow) {
-          tmem_ld32p(tS + 32, s + 32);
-          tmem_ld32p(tS + 64, s + 64);
-          tmem_ld32p(tS + 96, s + 96);
-        }
+        tmem_ld32p(tS + 32, s + 32);
+        c.next(a, w);
         tmem_ld_wait();
-        if (narrow) {
-#pragma unroll
-          for (int c = 32; c < 128; ++c) s[c] = __float_as_uint(-INFINITY);
-        }
         if (masked) {
+          // columns c <= hi and (c >= lo or c < sk) are visible
+          const int hi = p - key0, lo = a.window > 0 ? hi - a.window + 1 : INT_MIN, sk = a.sinks - key0;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t see =
-                low_bits(hi + 1 - 32 * x) & (~low_bits(lo - 32 * x) | low_bits(sk - 32 * x));
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t see = low_bits(hi + 1 - 32 * x) & (~low_bits(lo - 32 * x) | low_bits(sk - 32 * x));
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!((see >> c) & 1)) s[32 * x + c] = __float_as_uint(-INFINITY);
+            for (int e = 0; e < 32; ++e)
+              if (!((see >> e) & 1)) s[32 * x + e] = __float_as_uint(-INFINITY);
           }
         }
-        float mx8[8];
+        float mx4[4];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) mx8[c] = __uint_as_float(s[c]);
+        for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 4]));
 #pragma unroll
-        for (int c = 8; c < 128; c += 16)
+        for (int e = 8; e < kStep; e += 8)
 #pragma unroll
-          for (int x = 0; x < 8; ++x)
-            mx8[x] = c + 8 < 128 ? fmax3(mx8[x], __uint_as_float(s[c + x]), __uint_as_float(s[(c + 8 + x) & 127]))
-                                 : fmaxf(mx8[x], __uint_as_float(s[c + x]));
-        const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], fmax3(mx8[5], mx8[6], mx8[7])));
+          for (int x = 0; x < 4; ++x) mx4[x] = fmax3(mx4[x], __uint_as_float(s[e + x]), __uint_as_float(s[e + 4 + x]));
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         if (m == -INFINITY) m = mx;  // nothing visible before: l = 0 and O = 0 (or unset)
         const bool grow = mx > m + slack;
         if (__any_sync(0xffffffffu, grow)) {
           const float alpha = grow ? ex2_approx((m - mx) * scale) : 1.0f;
           if (grow) m = mx;
           l *= alpha;
-          if (!(ok = mbar_wait_warp(&bar.o_done[ti], (step - 1) & 1))) break;
+          if (!(ok = mbar_wait_warp(&bar.pv_done[ti], (step - 1) & 1))) break;
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            uint32_t x[16];
-            tmem_ld16p(tO + c, x);
+          for (int x = 0; x < D; x += 16) {
+            uint32_t o[16];
+            tmem_ld16p(tO + x, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
-            tmem_st16p(tO + c, x);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st16p(tO + x, o);
           }
         }
         const float ms = m == -INFINITY ? 0.0f : m * scale;
         const float2 sc = make_float2(scale, scale), off = make_float2(-ms, -ms);
         float2 sum[4] = {};
+        auto weights = [&](auto poly) {  // into P, over S
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) {
-          if (c > 0 && narrow) break;
-          uint32_t y[16];
+          for (int x = 0; x < kStep; x += 32) {
+            uint32_t y[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 u =
-                ffma2(make_float2(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1])), sc, off);
-            const float2 f = make_float2(ex2_approx(u.x), ex2_approx(u.y));
-            sum[(e / 2) & 3] = fadd2(sum[(e / 2) & 3], f);
-            y[e / 2] = pack16<T>(f.x, f.y);
+            for (int e = 0; e < 32; e += 2) {
+              const float2 u =
+                  ffma2(make_float2(__uint_as_float(s[x + e]), __uint_as_float(s[x + e + 1])), sc, off);
+              const float2 f = decltype(poly)::value && ((kWinPoly >> (e / 2)) & 1)
+                                   ? exp2_poly2(u)
+                                   : make_float2(ex2_approx(u.x), ex2_approx(u.y));
+              sum[(e / 2) & 3] = fadd2(sum[(e / 2) & 3], f);
+              y[e / 2] = pack16<T>(f.x, f.y);
+            }
+            tmem_st16p(tS + x / 2, y);
           }
-          tmem_st16p(tS + kP + c / 2, y);
-        }
+        };
+        if (masked) weights(std::false_type());  // (the polynomial gives 2^-126 for -inf)
+        else weights(std::true_type());
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_full[ti]);
+        if (lane == 0) mbar_arrive(&bar.p_full[2 * ti + (step & 1)]);
         const float2 t = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
         l += t.x + t.y;
       }
       if (!ok) break;
       // l and m for the output warps, once they have read the last item's
-      if (items > 0 && !(ok = mbar_wait_warp(&bar.o_free[ti], (items - 1) & 1))) break;
+      if (n_items > 0 && !(ok = mbar_wait_warp(&bar.o_free[ti], (n_items - 1) & 1))) break;
       s_l[128 * ti + row] = make_float2(l, m * scale);
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.l_ready[ti]);
-      ++items;
+      ++n_items;
     }
   } else {
     // ------------------------------------------------------------ output
-    regs_dec<kWinRegsOut>();
     const int quarter = warp & 3, row = quarter * 32 + lane;
     const bool wide = (reinterpret_cast<uintptr_t>(a.o) & 31) == 0;
-    uint32_t items[2] = {0, 0};
+    uint32_t n_items[2] = {0, 0};
     bool ok = true;
-    for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
-      const WinItem w = win_item(a, it);
-      for (int i = 0; i < 2 && ok; ++i) {
-        if (w.count(i) == 0) continue;
-        if (!(ok = mbar_wait_warp(&bar.l_ready[i], items[i] & 1))) break;
-        if (!(ok = mbar_wait_warp(&bar.o_full[i], items[i] & 1))) break;
+    WinItem w;
+    for (uint32_t nth = 0; ok && win_next(items, bar, nth, w); ++nth) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (!w.rows(i) || !ok) continue;
+        if (!(ok = mbar_wait_warp(&bar.l_ready[i], n_items[i] & 1))) break;
+        if (!(ok = mbar_wait_warp(&bar.o_full[i], n_items[i] & 1))) break;
         tc_fence_after();
-        ++items[i];
+        ++n_items[i];
         const float2 lm = s_l[128 * i + row];
         const int p = w.q0 + 128 * i + row;
         const float inv = 1.0f / lm.x;
@@ -591,7 +646,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
           uint32_t x[32];
           tmem_ld32p(tO + c, x);
           tmem_ld_wait();
-          if (c + 32 == D) {  // O_i is read
+          if (c + 32 == D) {  // O_i, l and m are read
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.o_free[i]);
@@ -610,7 +665,6 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         }
         if (a.lse && p < w.n) a.lse[head * a.N + p] = (lm.y + log2f(lm.x)) * 0.6931471805599453f;
         uint32_t redo = __ballot_sync(0xffffffffu, odd != 0.0f && p < w.n);
-        __syncwarp();
         for (; redo; redo &= redo - 1) window_row<T, D>(a, w.b, w.h, w.q0 + 128 * i + quarter * 32 + __ffs(redo) - 1);
       }
     }
@@ -644,23 +698,22 @@ cudaError_t launch_window_t(WindowArgs a, cudaStream_t st) {
   CUtensorMap q, k, v, kn, vn;
   if (!map_window(&q, a.q, D, a.N, a.Hq, a.B, a.nhd, 128) || !map_window(&k, a.k, D, a.N, a.Hkv, a.B, a.nhd, 128) ||
       !map_window(&v, a.v, D, a.N, a.Hkv, a.B, a.nhd, 128) ||
-      !map_window(&kn, a.k, D, a.N, a.Hkv, a.B, a.nhd, kNarrow) ||
-      !map_window(&vn, a.v, D, a.N, a.Hkv, a.B, a.nhd, kNarrow))
+      !map_window(&kn, a.k, D, a.N, a.Hkv, a.B, a.nhd, kStep) ||
+      !map_window(&vn, a.v, D, a.N, a.Hkv, a.B, a.nhd, kStep))
     return cudaErrorInvalidValue;
-  int dev = 0, sms = 0;
   cudaError_t e;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   auto kernel = attn_window_kernel<T, D>;
   if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, WinSmem<D>::kBytes)) != cudaSuccess)
     return e;
-  const int64_t items = (int64_t)a.B * a.Hq * ((a.N + 255) / 256);  // at most B Hq N < 2^31
-  a.items = (int)items;
-  // heads whose K and V (32 MB of the 126 MB L2) are in use at a time
-  const int64_t kv = (int64_t)a.N * D * 4 / (a.Hq / a.Hkv) + 1;
-  const int64_t group = (32 << 20) / kv;
-  a.group = (int)(group < 1 ? 1 : group > (int64_t)a.B * a.Hq ? (int64_t)a.B * a.Hq : group);
-  kernel<<<(unsigned)(items < sms ? items : sms), kWinThreads, WinSmem<D>::kBytes, st>>>(q, k, v, kn, vn, a);
+  const int64_t heads = (int64_t)a.B * a.Hq;
+  a.pairs = (a.N + 255) / 256;
+  a.items = (int)(heads * a.pairs);  // at most B Hq N < 2^31
+  // heads whose K and V (32 MB of the 126 MB L2) are in use at a time, in groups of one size
+  const int64_t kv = (int64_t)a.N * D * 4;
+  int64_t groups = (heads * kv / (a.Hq / a.Hkv) + (32 << 20) - 1) >> 25;
+  groups = groups < 1 ? 1 : groups > heads ? heads : groups;
+  a.group = (int)((heads + groups - 1) / groups);
+  kernel<<<(unsigned)a.items, kWinThreads, WinSmem<D>::kBytes, st>>>(q, k, v, kn, vn, a);
   return cudaGetLastError();
 }
 

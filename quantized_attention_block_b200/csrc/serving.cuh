@@ -77,7 +77,7 @@ struct WindowArgs {
   int B, Hq, Hkv, N, D;
   int nhd, window, sinks;
   float sm_scale, scale_log2;
-  int items, group;  // work items, and heads whose items follow one another (set at launch)
+  int items, pairs, group;  // set at launch: work items, row pairs of a head, heads whose items follow one another
 };
 
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t st);

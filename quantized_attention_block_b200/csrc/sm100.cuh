@@ -51,6 +51,17 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
 // ------------------------------------------------------------------ mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
@@ -355,6 +366,33 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// ------------------------------------------------------------------ work stealing
+// Asks for a CTA of this grid that has not started (cluster launch control): the
+// 16-byte answer lands in shared memory, counted in bytes on `bar`.  Not to be
+// asked again after a refusal.
+__device__ __forceinline__ void clc_try_cancel(void* answer, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(answer)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// Whether the request got a CTA (which then never starts), and its blockIdx.x
+__device__ __forceinline__ bool clc_answer(const void* answer, uint32_t& block_x) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(ok), "=r"(block_x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return ok != 0;
+}
+
 // Per-warpgroup register budget (all four warps of the warpgroup execute it).
 template <uint32_t N>
 __device__ __forceinline__ void regs_inc() {
@@ -443,8 +481,8 @@ constexpr float kExp2C0 = 0.9999977946281433f, kExp2C1 = 0.693130612373352f, kEx
 __device__ __forceinline__ float2 exp2_poly2(float2 x) {
   x = make_float2(fmaxf(x.x, -126.0f), fmaxf(x.y, -126.0f));
   const float2 j = __fadd2_rn(x, make_float2(12582912.0f, 12582912.0f));
-  const float2 n = __fadd2_rn(j, make_float2(-12582912.0f, -12582912.0f));
-  const float2 f = __fadd2_rn(x, make_float2(-n.x, -n.y));
+  const float2 minus_n = __ffma2_rn(j, make_float2(-1.0f, -1.0f), make_float2(12582912.0f, 12582912.0f));
+  const float2 f = __fadd2_rn(x, minus_n);
   float2 p = __ffma2_rn(f, make_float2(kExp2C4, kExp2C4), make_float2(kExp2C3, kExp2C3));
   p = __ffma2_rn(f, p, make_float2(kExp2C2, kExp2C2));
   p = __ffma2_rn(f, p, make_float2(kExp2C1, kExp2C1));
