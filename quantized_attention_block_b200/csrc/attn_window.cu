@@ -69,39 +69,29 @@ struct WinSmem {
 };
 
 // The key tiles of a work item: sink tiles [0, ns) with keys 128 j.., then the
-// tiles of the window, keys 128 (t0 + j - ns)..  Row tile i takes the sink tiles
-// and [lo(i), hi(i)], in steps of 64 keys.
+// tiles of the window, keys 128 (t0 + j - ns)...
 struct __align__(16) WinItem {
   int b, h, q0, n;
   int ns, t0, nt;  // nt: key tiles of the item; 0: no more items
-  int window;
-  __device__ __forceinline__ int lead(int i) const { return q0 + 128 * i - window + 1; }  // first key of the window
-  __device__ __forceinline__ int lo(int i) const { return ns + (t0 > 0 && lead(i) > 0 ? lead(i) / 128 : 0) - t0; }
-  __device__ __forceinline__ int hi(int i) const { return ns + q0 / 128 + i - t0; }
-  __device__ __forceinline__ bool rows(int i) const { return q0 + 128 * i < n; }
-  __device__ __forceinline__ int key0(int j) const { return 128 * (j < ns ? j : t0 + j - ns); }
+  int narrow;      // the sink tile that is loaded by half, or -1
 };
-// A walk over the steps of row tile i (j == nt: past the last).  Steps whose keys no row sees are left out.
-struct WinWalk {
-  int i, lo, hi, j, sub, end;  // the step's key tile and half; halves of the tile
-  __device__ __forceinline__ void enter(const WindowArgs& a, const WinItem& w, int t) {
-    if (t >= w.ns && t < lo) t = lo;
-    j = t > hi ? w.nt : t;
-    const int key0 = w.key0(j);
-    end = (j < w.ns ? a.sinks : w.n) - key0 <= kStep ? 1 : 2;
-    sub = j == lo && w.t0 > 0 && w.lead(i) - key0 >= kStep ? 1 : 0;
+// The steps of row tile i: halves u of key tiles (u / 2), from `first` on, `lo` after `sink`, up to `end`.
+// Steps whose keys no row sees are left out.
+struct WinSteps {
+  int first, sink, lo, end;
+  __device__ __forceinline__ WinSteps(const WindowArgs& a, const WinItem& w, int i) {
+    const int q0 = w.q0 + 128 * i, lead = q0 - a.window + 1;  // lead: first key of the window
+    const int tile = w.t0 > 0 && lead > 0 ? lead / 128 : 0;
+    lo = 2 * (w.ns + tile - w.t0) + (w.t0 > 0 && lead - 128 * tile >= kStep ? 1 : 0);
+    sink = w.ns > 0 ? (a.sinks + kStep - 1) / kStep : -1;
+    end = q0 < w.n ? 2 * (w.ns + q0 / 128 - w.t0) + (w.n - q0 <= kStep ? 1 : 2) : 0;
+    first = q0 < w.n ? (w.ns > 0 ? 0 : lo) : 0;
   }
-  __device__ __forceinline__ void begin(const WindowArgs& a, const WinItem& w, int tile) {
-    i = tile;
-    lo = w.lo(i);
-    hi = w.hi(i);
-    if (w.rows(i)) enter(a, w, 0);
-    else j = w.nt;
-  }
-  __device__ __forceinline__ void next(const WindowArgs& a, const WinItem& w) {
-    if (++sub >= end) enter(a, w, j + 1);
-  }
+  __device__ __forceinline__ int next(int u) const { return u + 1 == sink ? lo : u + 1; }
 };
+__device__ __forceinline__ int win_key(const WinItem& w, int u) {  // first key of a step
+  return kStep * u + (u >= 2 * w.ns ? 128 * (w.t0 - w.ns) : 0);
+}
 static_assert(sizeof(WinItem) == 32, "items are passed through shared memory as two 16-byte words");
 
 __device__ __forceinline__ WinItem win_item(const WindowArgs& a, uint32_t idx) {
@@ -114,17 +104,13 @@ __device__ __forceinline__ WinItem win_item(const WindowArgs& a, uint32_t idx) {
   w.h = bh - w.b * a.Hq;
   w.q0 = 256 * (a.pairs - 1 - (int)pair);
   w.n = a.lens ? min(max(__ldg(a.lens + w.b), 0), a.N) : a.N;
-  w.window = a.window;
   const int lead = w.q0 - a.window + 1;
   w.t0 = a.window > 0 && lead > 0 ? lead / 128 : 0;
   if (a.sinks > 128 * w.t0) w.t0 = 0;  // the sinks reach into the window's tiles: every tile from 0 on
   w.ns = w.t0 > 0 ? (a.sinks + 127) / 128 : 0;
-  w.nt = w.q0 >= w.n ? 0 : w.hi(w.q0 + 128 < w.n ? 1 : 0) + 1;
+  w.nt = w.q0 >= w.n ? 0 : w.ns + w.q0 / 128 - w.t0 + (w.q0 + 128 < w.n ? 2 : 1);
+  w.narrow = w.ns > 0 && a.sinks - 128 * (w.ns - 1) <= kStep ? w.ns - 1 : -1;
   return w;
-}
-// the last sink tile is loaded by half if that holds the sinks
-__device__ __forceinline__ bool win_narrow(const WindowArgs& a, const WinItem& w, int j) {
-  return j == w.ns - 1 && a.sinks - 128 * j <= kStep;
 }
 
 // One row by one warp, over its visible keys alone: lane = key for the scores,
@@ -251,7 +237,7 @@ __device__ __forceinline__ bool win_next(const WinItem* ring, const WinBars& bar
   const uint4* p = reinterpret_cast<const uint4*>(ring + s);
   const uint4 x = p[0], y = p[1];
   w.b = x.x, w.h = x.y, w.q0 = x.z, w.n = x.w;
-  w.ns = y.x, w.t0 = y.y, w.nt = y.z, w.window = y.w;
+  w.ns = y.x, w.t0 = y.y, w.nt = y.z, w.narrow = y.w;
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(&bar.item_empty[s]);
   return w.nt > 0;
@@ -346,8 +332,8 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         const int hk = w.h / G;
         for (int j = 0; j < w.nt && ok; ++j) {
           if (lane == 0 && j == max(0, w.nt - 4)) mbar_arrive(bar.item_want);
-          const bool narrow = win_narrow(a, w, j);
-          const int key0 = w.key0(j);
+          const bool narrow = j == w.narrow;
+          const int key0 = win_key(w, 2 * j);
           const uint32_t rows = narrow ? kStep : 128, bytes = rows * D * 2, half = rows * 128;
           for (int x = 0; x < 2 && ok; ++x, ++idx) {  // K, then V
             const uint32_t s = idx % R;
@@ -377,7 +363,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
             if (j == 0 && x == 0 && ok && lane == 0) {
               // Q after the first K: it waits for the last item's last product
               for (int i = 0; i < 2; ++i) {
-                if (!w.rows(i)) continue;
+                if (w.q0 + 128 * i >= w.n) continue;
                 if (nq[i] > 0 && !(ok = mbar_wait(&bar.q_empty[i], (nq[i] - 1) & 1))) break;
                 mbar_expect_tx(&bar.q_full[i], L::kTileBytes);
                 for (int c = 0; c < D / 64; ++c)
@@ -400,81 +386,104 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       // ------------------------------------------------------------ MMA issuer of row tile i
       const int i = warp - 13;
       const uint32_t tS = tmem + 128 * i, tO = tmem + 256 + D * i;
-      const uint32_t q = smem_u32(sQ + i * L::kTileBytes);
+      // operand descriptors: 128-byte swizzle, 8 rows every 1024 bytes; the address (16 bytes a unit) is added to
+      // the low word, whose upper half for V holds the distance of the slot's halves of 64 channels
+      constexpr uint64_t kDesc = make_sdesc(0, 1024, kSwizzle128B), kDescV = kDesc & ~(uint64_t)0xFFFF0000u;
+      constexpr uint32_t kSlot = L::kTileBytes / 16, kRows = kStep * 128 / 16;  // a slot; the rows of a step
+      const uint64_t q = kDesc + smem_u32(sQ + i * L::kTileBytes) / 16;
+      const uint32_t ring0 = smem_u32(ring) / 16;
       const bool one = elect_one();
-      uint32_t g0 = 0, n_items = 0;      // key tiles of the items before; items of this row tile
-      uint32_t s_qk = 0, s_pv = 0;       // steps issued
+      uint32_t s_qk = 0, s_pv = 0, n_items = 0;  // steps issued, items
       bool ok = true;
+      // the ring's slots of K (and V): position, parity; the key tile there; whether it has been waited for
+      struct Slots {
+        uint32_t at, parity;
+        int tile;
+        bool ready;
+        __device__ __forceinline__ void advance() {
+          at += 2;
+          if (at >= R) {
+            at -= R;
+            parity ^= 1;
+          }
+          ++tile;
+          ready = false;
+        }
+      } ks = {0, 0, 0, false}, vs = {1, 0, 0, false};
+      // on to key tile `to`; the tiles before it, which this row tile does not see, are released unread
+      auto skip = [&](Slots& s, int to) {
+        while (s.tile < to && ok) {
+          ok = mbar_wait_warp(&bar.kv_full[s.at], s.parity);
+          if (ok && lane == 0) mbar_arrive(&bar.kv_empty[s.at]);
+          s.advance();
+        }
+      };
+      auto ready = [&](Slots& s) {
+        if (!s.ready) s.ready = ok = mbar_wait_warp(&bar.kv_full[s.at], s.parity);
+        return ok;
+      };
       WinItem w;
       for (uint32_t nth = 0; ok && win_next(items, bar, nth, w); ++nth) {
-        // the slots of K (x = 0) or V (1) of key tiles [from, to), which this row tile does not see, released unread
-        auto pass = [&](int from, int to, uint32_t x) {
-          for (int j = from; j < to && ok; ++j) {
-            const uint32_t at = 2 * (g0 + j) + x;
-            ok = mbar_wait_warp(&bar.kv_full[at % R], (at / R) & 1);
-            if (ok && lane == 0) mbar_arrive(&bar.kv_empty[at % R]);
-          }
-        };
-        WinWalk c, d;  // the next S, the next P V
-        c.begin(a, w, i);
-        d = c;
-        pass(0, c.j, 0);
-        pass(0, d.j, 1);
-        if (w.rows(i)) {
-          ok = ok && mbar_wait_warp(&bar.q_full[i], n_items & 1);
-          bool first = true;
-          while (d.j < w.nt && ok) {
-            // S runs up to two steps ahead: its buffer was that of the P V before the last
-            while (c.j < w.nt && ok && s_qk < s_pv + 2) {
-              const uint32_t at = 2 * (g0 + c.j), slot = at % R;
-              if (!(ok = mbar_wait_warp(&bar.kv_full[slot], (at / R) & 1))) break;
-              tc_fence_after();
-              const int j = c.j, sub = c.sub;
-              const uint32_t half = (win_narrow(a, w, j) ? kStep : 128) * 128;  // bytes of 64 channels of the slot
-              c.next(a, w);
-              if (one) {
-                const uint32_t kt = smem_u32(ring + slot * L::kTileBytes) + sub * kStep * 128;
-                const uint32_t dst = tS + 64 * (s_qk & 1);
-#pragma unroll
-                for (int x = 0; x < D / 16; ++x)
-                  mma_f16(dst, make_sdesc(q + (x / 4) * 16384 + (x % 4) * 32, 1024, kSwizzle128B),
-                          make_sdesc(kt + (x / 4) * half + (x % 4) * 32, 1024, kSwizzle128B), kIdescQK, x > 0);
-                mma_commit(&bar.s_full[2 * i + (s_qk & 1)]);
-                if (c.j != j) mma_commit(&bar.kv_empty[slot]);
-                if (c.j == w.nt) mma_commit(&bar.q_empty[i]);
-              }
-              __syncwarp();
-              ++s_qk;
-              if (c.j > j + 1) pass(j + 1, c.j, 0);
-            }
-            if (!ok) break;
-            // O += P V: 16 keys are 8 columns of P and 16 rows of V
-            const uint32_t at = 2 * (g0 + d.j) + 1, slot = at % R;
-            if (!(ok = mbar_wait_warp(&bar.kv_full[slot], (at / R) & 1))) break;
-            if (first && n_items > 0 && !(ok = mbar_wait_warp(&bar.o_free[i], (n_items - 1) & 1))) break;
-            if (!(ok = mbar_wait_warp(&bar.p_full[2 * i + (s_pv & 1)], (s_pv >> 1) & 1))) break;
+        const WinSteps st(a, w, i);
+        const bool rows = st.end > 0;
+        ks.tile = vs.tile = 0;
+        skip(ks, rows ? st.first >> 1 : w.nt);
+        skip(vs, rows ? st.first >> 1 : w.nt);
+        if (!rows) continue;
+        ok = ok && mbar_wait_warp(&bar.q_full[i], n_items & 1);
+        int c = st.first, d = st.first;  // the next S, the next P V
+        while (d != st.end && ok) {
+          // S runs up to two steps ahead: its buffer was that of the P V before the last
+          while (c != st.end && s_qk < s_pv + 2 && ready(ks)) {
+            const int next = st.next(c);
+            const bool last = next == st.end, done = last || (next ^ c) > 1;  // of the item, of the key tile
             tc_fence_after();
-            const int j = d.j, sub = d.sub;
-            const uint32_t half = (win_narrow(a, w, j) ? kStep : 128) * 128;
-            d.next(a, w);
             if (one) {
-              const uint32_t vt = smem_u32(ring + slot * L::kTileBytes) + sub * kStep * 128;
+              const uint64_t k = kDesc + ring0 + ks.at * kSlot + (c & 1) * kRows;
+              const uint32_t half = (ks.tile == w.narrow ? kStep : 128) * 128 / 16;  // between the slot's halves
+              const uint32_t dst = tS + 64 * (s_qk & 1);
 #pragma unroll
-              for (int x = 0; x < kStep / 16; ++x)
-                mma_f16_ts(tO, tS + 64 * (s_pv & 1) + 8 * x, make_sdesc_mn(vt + x * 2048, half, 1024, kSwizzle128B),
-                           kIdescPV, !first || x > 0);
-              mma_commit(&bar.pv_done[i]);
-              if (d.j != j) mma_commit(&bar.kv_empty[slot]);
-              if (d.j == w.nt) mma_commit(&bar.o_full[i]);
+              for (int x = 0; x < D / 16; ++x)
+                mma_f16(dst, q + (x / 4) * 1024 + (x % 4) * 2, k + (x / 4) * half + (x % 4) * 2, kIdescQK, x > 0);
+              mma_commit(&bar.s_full[2 * i + (s_qk & 1)]);
+              if (done) mma_commit(&bar.kv_empty[ks.at]);
+              if (last) mma_commit(&bar.q_empty[i]);
             }
             __syncwarp();
-            ++s_pv;
-            first = false;
-            if (d.j > j + 1) pass(j + 1, d.j, 1);
+            ++s_qk;
+            c = next;
+            if (done) {
+              ks.advance();
+              skip(ks, last ? w.nt : next >> 1);
+            }
           }
-          ++n_items;
+          if (!ok || !ready(vs)) break;
+          if (d == st.first && n_items > 0 && !(ok = mbar_wait_warp(&bar.o_free[i], (n_items - 1) & 1))) break;
+          if (!(ok = mbar_wait_warp(&bar.p_full[2 * i + (s_pv & 1)], (s_pv >> 1) & 1))) break;
+          // O += P V: 16 keys are 8 columns of P and 16 rows of V
+          const int next = st.next(d);
+          const bool last = next == st.end, done = last || (next ^ d) > 1;
+          tc_fence_after();
+          if (one) {
+            const uint32_t half = (vs.tile == w.narrow ? kStep : 128) * 128 / 16;
+            const uint64_t v = kDescV + (half << 16) + ring0 + vs.at * kSlot + (d & 1) * kRows;
+            const uint32_t p = tS + 64 * (s_pv & 1);
+#pragma unroll
+            for (int x = 0; x < kStep / 16; ++x)
+              mma_f16_ts(tO, p + 8 * x, v + x * 128, kIdescPV, d != st.first || x > 0);
+            mma_commit(&bar.pv_done[i]);
+            if (done) mma_commit(&bar.kv_empty[vs.at]);
+            if (last) mma_commit(&bar.o_full[i]);
+          }
+          __syncwarp();
+          ++s_pv;
+          d = next;
+          if (done) {
+            vs.advance();
+            skip(vs, last ? w.nt : next >> 1);
+          }
         }
-        g0 += w.nt;
+        ++n_items;
       }
       // every tensor-core op retired before TMEM is released
       if (one) {
@@ -527,23 +536,21 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     bool ok = true;
     WinItem w;
     for (uint32_t nth = 0; ok && win_next(items, bar, nth, w); ++nth) {
-      if (!w.rows(ti)) continue;
+      const WinSteps st(a, w, ti);
+      if (st.end == 0) continue;
       const int p0 = w.q0 + 128 * ti, p = p0 + row;
       float m = -INFINITY, l = 0.0f;
-      WinWalk c;
-      c.begin(a, w, ti);
-      for (; c.j < w.nt; ++step) {
+      for (int u = st.first; u != st.end; u = st.next(u), ++step) {
         const uint32_t tS = tmem + 128 * ti + 64 * (step & 1) + lanes;
-        const int key0 = w.key0(c.j) + kStep * c.sub;
-        const int end = c.j < w.ns ? a.sinks - key0 : INT_MAX;  // columns of a sink tile that are sinks
-        const bool masked = end < kStep || key0 + kStep - 1 > p0 ||
-                            (a.window > 0 && c.j >= w.ns && p0 + 128 - a.window > key0 && a.sinks - key0 < kStep);
+        const int key0 = win_key(w, u);
+        // keys behind the first row's position, before the last row's window, or behind the sinks
+        const bool masked = key0 + kStep - 1 > p0 ||
+                            (a.window > 0 && p0 + 128 - a.window > key0 && a.sinks - key0 < kStep);
         if (!(ok = mbar_wait_warp(&bar.s_full[2 * ti + (step & 1)], (step >> 1) & 1))) break;
         tc_fence_after();
         uint32_t s[kStep];
         tmem_ld32p(tS, s);
         tmem_ld32p(tS + 32, s + 32);
-        c.next(a, w);
         tmem_ld_wait();
         if (masked) {
           // columns c <= hi and (c >= lo or c < sk) are visible
@@ -629,7 +636,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     for (uint32_t nth = 0; ok && win_next(items, bar, nth, w); ++nth) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if (!w.rows(i) || !ok) continue;
+        if (w.q0 + 128 * i >= w.n || !ok) continue;
         if (!(ok = mbar_wait_warp(&bar.l_ready[i], n_items[i] & 1))) break;
         if (!(ok = mbar_wait_warp(&bar.o_full[i], n_items[i] & 1))) break;
         tc_fence_after();

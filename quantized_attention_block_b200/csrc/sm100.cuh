@@ -408,25 +408,12 @@ __device__ __forceinline__ void regs_dec() {
 // stride byte offsets (>> 4), version 1 at bit 46, swizzle mode at bits 61-63.
 enum : uint32_t { kSwizzleNone = 0, kSwizzle128B = 2, kSwizzle64B = 4, kSwizzle32B = 6 };
 
-__device__ __forceinline__ uint64_t make_sdesc(uint32_t saddr, uint32_t sbo_bytes, uint32_t swizzle) {
+__host__ __device__ constexpr uint64_t make_sdesc(uint32_t saddr, uint32_t sbo_bytes, uint32_t swizzle) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(1u) << 16;                    // LBO: unused for swizzled K-major
+  d |= static_cast<uint64_t>(1u) << 16;                    // LBO: unused for swizzled K-major; else the distance of atoms along M / N
   d |= static_cast<uint64_t>((sbo_bytes >> 4) & 0x3FFFu) << 32;
   d |= static_cast<uint64_t>(1u) << 46;                    // descriptor version (sm_100)
-  d |= static_cast<uint64_t>(swizzle & 7u) << 61;
-  return d;
-}
-
-// An operand whose M / N dimension is contiguous (rows of K): swizzle atoms of 8
-// rows; `lbo` bytes between atoms along M / N, `sbo` between groups of 8 rows.
-__device__ __forceinline__ uint64_t make_sdesc_mn(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes,
-                                                  uint32_t swizzle) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>((lbo_bytes >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>((sbo_bytes >> 4) & 0x3FFFu) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
   d |= static_cast<uint64_t>(swizzle & 7u) << 61;
   return d;
 }
