@@ -227,19 +227,20 @@ struct WinBars {
 };
 constexpr int kItemReaders = 15;
 
+// A value that all lanes of the warp hold, known to be so: what it addresses can stay in uniform registers.  (An MMA
+// whose descriptors come from per-thread registers takes some 100 cycles to issue, twice its run time.)
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // The next item, from the ring that the taking warp fills: false without one (w.nt == 0) or if the wait gave up
-// One thread of the warp reads it (ONE) or all of them.
-template <bool ONE = false>
 __device__ __forceinline__ bool win_next(const WinItem* ring, const WinBars& bar, uint32_t nth, WinItem& w) {
   const uint32_t s = nth & 1;
-  if (!(ONE ? mbar_wait(&bar.item_full[s], (nth >> 1) & 1) : mbar_wait_warp(&bar.item_full[s], (nth >> 1) & 1)))
-    return false;
+  if (!mbar_wait_warp(&bar.item_full[s], (nth >> 1) & 1)) return false;
   const uint4* p = reinterpret_cast<const uint4*>(ring + s);
   const uint4 x = p[0], y = p[1];
-  w.b = x.x, w.h = x.y, w.q0 = x.z, w.n = x.w;
-  w.ns = y.x, w.t0 = y.y, w.nt = y.z, w.narrow = y.w;
-  if (!ONE) __syncwarp();
-  if (ONE || (threadIdx.x & 31) == 0) mbar_arrive(&bar.item_empty[s]);
+  w.b = uniform(x.x), w.h = uniform(x.y), w.q0 = uniform(x.z), w.n = uniform(x.w);
+  w.ns = uniform(y.x), w.t0 = uniform(y.y), w.nt = uniform(y.z), w.narrow = uniform(y.w);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&bar.item_empty[s]);
   return w.nt > 0;
 }
 
@@ -384,106 +385,113 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       }
     } else if (warp < 15) {
       // ------------------------------------------------------------ MMA issuer of row tile i
-      const int i = warp - 13;
-      const uint32_t tS = tmem + 128 * i, tO = tmem + 256 + D * i;
+      const int i = uniform(warp) - 13;
+      const uint32_t base = uniform(tmem), tS = base + 128 * i, tO = base + 256 + D * i;
       // operand descriptors: 128-byte swizzle, 8 rows every 1024 bytes; the address (16 bytes a unit) is added to
       // the low word, whose upper half for V holds the distance of the slot's halves of 64 channels
-      constexpr uint64_t kDesc = make_sdesc(0, 1024, kSwizzle128B), kDescV = kDesc & ~(uint64_t)0xFFFF0000u;
+      constexpr uint32_t kHi = make_sdesc(0, 1024, kSwizzle128B) >> 32, kLo = 1u << 16;
       constexpr uint32_t kSlot = L::kTileBytes / 16, kRows = kStep * 128 / 16;  // a slot; the rows of a step
-      const uint64_t q = kDesc + smem_u32(sQ + i * L::kTileBytes) / 16;
+      const uint32_t q = kLo + smem_u32(sQ + i * L::kTileBytes) / 16;
       const uint32_t ring0 = smem_u32(ring) / 16;
-      if (lane == 0) {
-        uint32_t s_qk = 0, s_pv = 0, n_items = 0;  // steps issued, items
-        bool ok = true;
-        // the ring's slots of K (and V): position, parity; the key tile there; whether it has been waited for
-        struct Slots {
-          uint32_t at, parity;
-          int tile;
-          bool ready;
-          __device__ __forceinline__ void advance() {
-            at += 2;
-            if (at >= R) {
-              at -= R;
-              parity ^= 1;
-            }
-            ++tile;
-            ready = false;
+      uint32_t s_qk = 0, s_pv = 0, n_items = 0;  // steps issued, items
+      bool ok = true;
+      // the ring's slots of K (and V): position, parity; the key tile there; whether it has been waited for
+      struct Slots {
+        uint32_t at, parity;
+        int tile;
+        bool ready;
+        __device__ __forceinline__ void advance() {
+          at += 2;
+          if (at >= R) {
+            at -= R;
+            parity ^= 1;
           }
-        } ks = {0, 0, 0, false}, vs = {1, 0, 0, false};
-        // on to key tile `to`; the tiles before it, which this row tile does not see, are released unread
-        auto skip = [&](Slots& s, int to) {
-          while (s.tile < to && ok) {
-            ok = mbar_wait(&bar.kv_full[s.at], s.parity);
-            if (ok) mbar_arrive(&bar.kv_empty[s.at]);
-            s.advance();
-          }
-        };
-        auto ready = [&](Slots& s) {
-          if (!s.ready) s.ready = ok = mbar_wait(&bar.kv_full[s.at], s.parity);
-          return ok;
-        };
-        WinItem w;
-        for (uint32_t nth = 0; ok && win_next<true>(items, bar, nth, w); ++nth) {
-          const WinSteps st(a, w, i);
-          const bool rows = st.end > 0;
-          ks.tile = vs.tile = 0;
-          skip(ks, rows ? st.first >> 1 : w.nt);
-          skip(vs, rows ? st.first >> 1 : w.nt);
-          if (!rows) continue;
-          ok = ok && mbar_wait(&bar.q_full[i], n_items & 1);
-          int c = st.first, d = st.first;  // the next S, the next P V
-          auto qk = [&] {  // S = Q K^T of step c
-            const int next = st.next(c);
-            const bool last = next == st.end, done = last || (next ^ c) > 1;  // of the item, of the key tile
-            const uint64_t k = kDesc + ring0 + ks.at * kSlot + (c & 1) * kRows;
-            const uint32_t half = (ks.tile == w.narrow ? kStep : 128) * 128 / 16;  // between the slot's halves
-            const uint32_t dst = tS + 64 * (s_qk & 1);
+          ++tile;
+          ready = false;
+        }
+      } ks = {0, 0, 0, false}, vs = {1, 0, 0, false};
+      // on to key tile `to`; the tiles before it, which this row tile does not see, are released unread
+      auto skip = [&](Slots& s, int to) {
+        while (s.tile < to && ok) {
+          ok = mbar_wait_warp(&bar.kv_full[s.at], s.parity);
+          if (ok && lane == 0) mbar_arrive(&bar.kv_empty[s.at]);
+          s.advance();
+        }
+      };
+      auto ready = [&](Slots& s) {
+        if (!s.ready) s.ready = ok = mbar_wait_warp(&bar.kv_full[s.at], s.parity);
+        return ok;
+      };
+      WinItem w;
+      for (uint32_t nth = 0; ok && win_next(items, bar, nth, w); ++nth) {
+        const WinSteps st(a, w, i);
+        const bool rows = st.end > 0;
+        ks.tile = vs.tile = 0;
+        skip(ks, rows ? st.first >> 1 : w.nt);
+        skip(vs, rows ? st.first >> 1 : w.nt);
+        if (!rows) continue;
+        ok = ok && mbar_wait_warp(&bar.q_full[i], n_items & 1);
+        int c = st.first, d = st.first;  // the next S, the next P V
+        auto qk = [&] {  // S = Q K^T of step c
+          const int next = st.next(c);
+          const bool last = next == st.end, done = last || (next ^ c) > 1;  // of the item, of the key tile
+          const uint32_t k = kLo + ring0 + ks.at * kSlot + (c & 1) * kRows;
+          const uint32_t half = (ks.tile == w.narrow ? kStep : 128) * 128 / 16;  // between the slot's halves
+          const uint32_t dst = tS + 64 * (s_qk & 1);
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
             for (int x = 0; x < D / 16; ++x)
-              mma_f16(dst, q + (x / 4) * 1024 + (x % 4) * 2, k + (x / 4) * half + (x % 4) * 2, kIdescQK, x > 0);
+              mma_f16(dst, q + (x / 4) * 1024 + (x % 4) * 2, k + (x / 4) * half + (x % 4) * 2, kHi, kIdescQK, x > 0);
             mma_commit(&bar.s_full[2 * i + (s_qk & 1)]);
             if (done) mma_commit(&bar.kv_empty[ks.at]);
             if (last) mma_commit(&bar.q_empty[i]);
-            ++s_qk;
-            c = next;
-            if (done) {
-              ks.advance();
-              skip(ks, last ? w.nt : next >> 1);
-            }
-          };
-          for (int x = 0; x < 2 && ok && c != st.end && ready(ks); ++x) qk();
-          if (ok && n_items > 0) ok = mbar_wait(&bar.o_free[i], (n_items - 1) & 1);
-          while (d != st.end && ok) {
-            if (!ready(vs)) break;
-            const int next = st.next(d);
-            const bool last = next == st.end, done = last || (next ^ d) > 1;
-            const uint32_t half = (vs.tile == w.narrow ? kStep : 128) * 128 / 16;
-            const uint64_t v = kDescV + (half << 16) + ring0 + vs.at * kSlot + (d & 1) * kRows;
-            const uint32_t p = tS + 64 * (s_pv & 1);
-            if (!(ok = mbar_wait(&bar.p_full[2 * i + (s_pv & 1)], (s_pv >> 1) & 1))) break;
-            tc_fence_after();
-            // O += P V: 16 keys are 8 columns of P and 16 rows of V
+          }
+          __syncwarp();
+          ++s_qk;
+          c = next;
+          if (done) {
+            ks.advance();
+            skip(ks, last ? w.nt : next >> 1);
+          }
+        };
+        for (int x = 0; x < 2 && ok && c != st.end && ready(ks); ++x) qk();
+        if (ok && n_items > 0) ok = mbar_wait_warp(&bar.o_free[i], (n_items - 1) & 1);
+        while (d != st.end && ok) {
+          if (!ready(vs)) break;
+          const int next = st.next(d);
+          const bool last = next == st.end, done = last || (next ^ d) > 1;
+          const uint32_t half = (vs.tile == w.narrow ? kStep : 128) * 128 / 16;
+          const uint32_t v = (half << 16) + ring0 + vs.at * kSlot + (d & 1) * kRows;
+          const uint32_t p = tS + 64 * (s_pv & 1);
+          if (!(ok = mbar_wait_warp(&bar.p_full[2 * i + (s_pv & 1)], (s_pv >> 1) & 1))) break;
+          tc_fence_after();
+          // O += P V: 16 keys are 8 columns of P and 16 rows of V
+          if (elect_one()) {
 #pragma unroll
             for (int x = 0; x < kStep / 16; ++x)
-              mma_f16_ts(tO, p + 8 * x, v + x * 128, kIdescPV, d != st.first || x > 0);
+              mma_f16_ts(tO, p + 8 * x, v + x * 128, kHi, kIdescPV, d != st.first || x > 0);
             mma_commit(&bar.pv_done[i]);
             if (done) mma_commit(&bar.kv_empty[vs.at]);
             if (last) mma_commit(&bar.o_full[i]);
-            // the S that takes P's buffer (not waited for before: the ring may not hold its K until V is free)
-            if (c != st.end) {
-              if (!ready(ks)) break;
-              qk();
-            }
-            ++s_pv;
-            d = next;
-            if (done) {
-              vs.advance();
-              skip(vs, last ? w.nt : next >> 1);
-            }
           }
-          ++n_items;
+          __syncwarp();
+          // the S that takes P's buffer (not waited for before: the ring may not hold its K until V is free)
+          if (c != st.end) {
+            if (!ready(ks)) break;
+            qk();
+          }
+          ++s_pv;
+          d = next;
+          if (done) {
+            vs.advance();
+            skip(vs, last ? w.nt : next >> 1);
+          }
         }
-        // every tensor-core op retired before TMEM is released
+        ++n_items;
+      }
+      // every tensor-core op retired before TMEM is released
+      if (elect_one()) {
         mma_commit(&bar.mma_done[i]);
         mbar_wait(&bar.mma_done[i], 0);
       }
