@@ -511,6 +511,7 @@ typedef struct {
     int32_t layout;            /* sage_layout of q, k, v and o */
     int32_t window, sinks;     /* window >= 1 (or 0: causal without a window), sinks >= 0 */
     float   sm_scale;          /* <= 0 selects 1/sqrt(d) */
+    int32_t zero_tail;         /* with lens, rows i >= lens[b]: bit 0 sets those of o to zero, bit 1 those of lse */
 } sage_window_params;
 
 /*
@@ -518,8 +519,8 @@ typedef struct {
  * of a model), in the inputs' 16-bit type, with fp32 sums and softmax.
  * q, k, v, o: device, contiguous, in the layout of p.  lse: device fp32
  * [B, Hq, N] or NULL.  lens: device [B] or NULL (N for every sequence): rows
- * i >= lens[b] of o and lse are left as they are and of k, v are not used
- * (values outside [0, N] are taken as the nearest bound).  A key that a row does
+ * i >= lens[b] of o and lse are left as they are (p->zero_tail: set to zero) and
+ * of k, v are not used (values outside [0, N] are taken as the nearest bound).  A key that a row does
  * not see has no influence on that row, whatever it holds.
  */
 SAGE_API sage_status sage_attn_window_fwd(const void *q, const void *k, const void *v, void *o, float *lse,

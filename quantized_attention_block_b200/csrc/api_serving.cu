@@ -66,9 +66,12 @@ sage_status check_decode(const sage_kv_cache* c, const sage_kv_seqs* s, const sa
   return SAGE_OK;
 }
 
+int group_tiles(int G) { return G <= 8 ? 1 : (G + kMaxGroup - 1) / kMaxGroup; }
+
 struct DecodeLayout {
   size_t prefix, part_m, part_l, part_o, lse2, scores, total;
   int64_t score_cap;
+  bool direct;
 };
 
 DecodeLayout decode_layout(const sage_kv_cache* c, const sage_kv_seqs* s, const sage_decode_params* p) {
@@ -79,16 +82,15 @@ DecodeLayout decode_layout(const sage_kv_cache* c, const sage_kv_seqs* s, const 
     off = align_up(off + bytes, 256);
     return o;
   };
-  L.prefix = take(8 * ((size_t)s->B + 1));
-  L.part_m = take(4 * (size_t)(2 * kDecodeCtas * kMaxGroup));
-  L.part_l = take(4 * (size_t)(2 * kDecodeCtas * kMaxGroup));
-  L.part_o = take(4 * (size_t)(2 * kDecodeCtas * kMaxGroup) * c->d);
+  const int64_t blocks = most_blocks((int64_t)s->max_pages * c->page_size, p->window, p->sinks);
+  L.direct = decode_direct((int64_t)s->B * c->Hkv * group_tiles(p->Hq / c->Hkv), blocks);
+  L.prefix = take(L.direct ? 1 : 8 * ((size_t)s->B + 1));
+  if (!L.direct) {
+    L.part_m = take(4 * (size_t)(2 * kDecodeCtas * kMaxGroup));
+    L.part_l = take(4 * (size_t)(2 * kDecodeCtas * kMaxGroup));
+    L.part_o = take(4 * (size_t)(2 * kDecodeCtas * kMaxGroup) * c->d);
+  }
   if (c->weight) {
-    int64_t blocks = ((int64_t)s->max_pages * c->page_size + kBlk - 1) / kBlk;
-    if (p->window > 0) {  // the blocks that a window and sinks can touch
-      const int64_t seen = (int64_t)p->window / kBlk + 2 + ((int64_t)p->sinks + kBlk - 1) / kBlk;
-      if (seen < blocks) blocks = seen;
-    }
     L.score_cap = blocks * kBlk;
     L.lse2 = take(4 * (size_t)s->B * p->Hq);
     L.scores = take(4 * (size_t)s->B * p->Hq * (size_t)L.score_cap);
@@ -154,7 +156,8 @@ sage_status sage_attn_decode(const void* q, void* o, float* lse, const float* km
   a.km = km;
   a.Hq = p->Hq;
   a.G = p->Hq / c->Hkv;
-  a.GT = a.G <= 8 ? 1 : (a.G + kMaxGroup - 1) / kMaxGroup;
+  a.GT = group_tiles(a.G);
+  a.direct = L.direct;
   a.window = p->window;
   a.sinks = p->sinks;
   a.q_fp16 = c->dtype == SAGE_FP16;
@@ -206,7 +209,7 @@ sage_status sage_attn_window_fwd(const void* q, const void* k, const void* v, vo
   if (p->d != 64 && p->d != 128) return SAGE_ERR_UNSUPPORTED_HEADDIM;
   if (p->dtype != SAGE_BF16 && p->dtype != SAGE_FP16) return SAGE_ERR_UNSUPPORTED_DTYPE;
   if (p->layout != SAGE_HND && p->layout != SAGE_NHD) return SAGE_ERR_INVALID_ARG;
-  if (p->window < 0 || p->sinks < 0) return SAGE_ERR_INVALID_ARG;
+  if (p->window < 0 || p->sinks < 0 || (p->zero_tail & ~3)) return SAGE_ERR_INVALID_ARG;
   if (std::isnan(p->sm_scale) || std::isinf(p->sm_scale)) return SAGE_ERR_INVALID_ARG;
   if ((int64_t)p->B * p->Hq * p->N >= (int64_t(1) << 31)) return SAGE_ERR_INVALID_ARG;
   if (!q || !k || !v || !o) return SAGE_ERR_INVALID_ARG;
@@ -230,6 +233,7 @@ sage_status sage_attn_window_fwd(const void* q, const void* k, const void* v, vo
   a.nhd = p->layout == SAGE_NHD;
   a.window = p->window;
   a.sinks = p->sinks;
+  a.zero_tail = lens ? p->zero_tail : 0;
   a.sm_scale = scale_or_default(p->sm_scale, p->d);
   a.scale_log2 = (float)((double)a.sm_scale * 1.4426950408889634);
   return from_cuda(launch_attn_window(a, p->dtype == SAGE_FP16, static_cast<cudaStream_t>(stream)));

@@ -69,7 +69,7 @@ struct WinSmem {
 // tiles of the window, keys 128 (t0 + j - ns)...
 struct __align__(16) WinItem {
   int b, h, q0, n;
-  int ns, t0, nt;  // nt: key tiles of the item; 0: no more items
+  int ns, t0, nt;  // nt: key tiles of the item; 0: its rows are behind the sequence; -1: no more items
   int narrow;      // the sink tile that is loaded by half, or -1
 };
 // The steps of row tile i: halves u of key tiles (u / 2), from `first` on, `lo` after `sink`, up to `end`.
@@ -231,7 +231,7 @@ constexpr int kItemReaders = 15;
 // whose descriptors come from per-thread registers takes some 100 cycles to issue, twice its run time.)
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-// The next item, from the ring that the taking warp fills: false without one (w.nt == 0) or if the wait gave up
+// The next item, from the ring that the taking warp fills: false without one or if the wait gave up
 __device__ __forceinline__ bool win_next(const WinItem* ring, const WinBars& bar, uint32_t nth, WinItem& w) {
   const uint32_t s = nth & 1;
   if (!mbar_wait_warp(&bar.item_full[s], (nth >> 1) & 1)) return false;
@@ -241,7 +241,7 @@ __device__ __forceinline__ bool win_next(const WinItem* ring, const WinBars& bar
   w.ns = uniform(y.x), w.t0 = uniform(y.y), w.nt = uniform(y.z), w.narrow = uniform(y.w);
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(&bar.item_empty[s]);
-  return w.nt > 0;
+  return w.nt >= 0;
 }
 
 template <typename T, int D>
@@ -331,6 +331,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       WinItem w;
       for (uint32_t nth = 0; ok && win_next(items, bar, nth, w); ++nth) {
         const int hk = w.h / G;
+        if (lane == 0 && w.nt == 0) mbar_arrive(bar.item_want);
         for (int j = 0; j < w.nt && ok; ++j) {
           if (lane == 0 && j == max(0, w.nt - 4)) mbar_arrive(bar.item_want);
           const bool narrow = j == w.narrow;
@@ -514,10 +515,11 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       };
       for (uint32_t nth = 0;; ++nth) {
         WinItem w;
-        w.nt = 0;
+        w.nt = -1;
         while (have) {
           w = win_item(a, idx);
-          if (w.nt > 0) break;
+          if (w.nt > 0 || a.zero_tail) break;
+          w.nt = -1;
           ask();  // (an item without rows is passed over)
         }
         if (nth >= 2 && !mbar_wait_warp(&bar.item_empty[nth & 1], ((nth >> 1) - 1) & 1)) break;
@@ -525,7 +527,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
           items[nth & 1] = w;
           mbar_arrive(&bar.item_full[nth & 1]);
         }
-        if (w.nt == 0) break;
+        if (w.nt < 0) break;
         // not before the item is nearly done: an item taken early is one that an idle CTA cannot take
         if (!mbar_wait_warp(bar.item_want, nth & 1)) break;
         ask();
@@ -634,16 +636,22 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     for (uint32_t nth = 0; ok && win_next(items, bar, nth, w); ++nth) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
+        const int p = w.q0 + 128 * i + row;
+        const int64_t head = (int64_t)w.b * a.Hq + w.h;
+        uint8_t* out = static_cast<uint8_t*>(a.o) + 2 * row_offset(head, p, a.Hq, a.N, D, a.nhd);
+        if (a.zero_tail && p >= w.n && p < a.N) {
+          if (a.zero_tail & 1)
+            for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(out + 2 * c) = make_uint4(0, 0, 0, 0);
+          if ((a.zero_tail & 2) && a.lse) a.lse[head * a.N + p] = 0.0f;
+        }
+        __syncwarp();
         if (w.q0 + 128 * i >= w.n || !ok) continue;
         if (!(ok = mbar_wait_warp(&bar.l_ready[i], n_items[i] & 1))) break;
         if (!(ok = mbar_wait_warp(&bar.o_full[i], n_items[i] & 1))) break;
         tc_fence_after();
         ++n_items[i];
         const float2 lm = s_l[128 * i + row];
-        const int p = w.q0 + 128 * i + row;
         const float inv = 1.0f / lm.x;
-        const int64_t head = (int64_t)w.b * a.Hq + w.h;
-        uint8_t* out = static_cast<uint8_t*>(a.o) + 2 * row_offset(head, p, a.Hq, a.N, D, a.nhd);
         const uint32_t tO = tmem + 256 + D * i + ((uint32_t)(quarter * 32) << 16);
         float odd = 0.0f;  // NaN once a value is not finite
 #pragma unroll
@@ -706,10 +714,12 @@ cudaError_t launch_window_t(WindowArgs a, cudaStream_t st) {
       !map_window(&kn, a.k, D, a.N, a.Hkv, a.B, a.nhd, kStep) ||
       !map_window(&vn, a.v, D, a.N, a.Hkv, a.B, a.nhd, kStep))
     return cudaErrorInvalidValue;
-  cudaError_t e;
   auto kernel = attn_window_kernel<T, D>;
-  if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, WinSmem<D>::kBytes)) != cudaSuccess)
-    return e;
+  static DeviceOnce once;
+  const cudaError_t e = once.run([&](int) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, WinSmem<D>::kBytes);
+  });
+  if (e != cudaSuccess) return e;
   const int64_t heads = (int64_t)a.B * a.Hq;
   a.pairs = (a.N + 255) / 256;
   a.items = (int)(heads * a.pairs);  // at most B Hq N < 2^31

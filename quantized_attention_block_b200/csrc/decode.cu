@@ -168,6 +168,20 @@ __device__ __forceinline__ void write_lse(const DecodeArgs& a, int b, int hq, fl
   }
 }
 
+// weight of the i-th visible slot of (b, h) += sum over the group's heads of 2^(t - lse2)
+template <typename F>
+__device__ __forceinline__ void add_weight(const DecodeArgs& a, const Span& sp, int b, int h, int i, F lse2) {
+  const int page = 1 << a.c.page_log2;
+  const int j = span_block(sp, i / kBlk) * kBlk + i % kBlk;
+  if (j >= sp.n || (j < sp.ws && j >= a.sinks)) return;
+  const int pid = a.c.table[(int64_t)b * a.c.max_pages + (j >> a.c.page_log2)];
+  if (pid < 0 || pid >= a.c.n_pages) return;
+  const float* t = a.scores + ((int64_t)b * a.Hq + h * a.G) * a.score_cap + i;
+  float x = 0.0f;
+  for (int g = 0; g < a.G; ++g) x += exp2f(t[g * a.score_cap] - lse2(g));
+  a.c.weight[((int64_t)pid * a.c.H + h) * page + (j & (page - 1))] += x;
+}
+
 // register i of Q's fragment; with 8 heads a row, rows 8-15 are zeros
 template <int MT, int I, int N>
 __device__ __forceinline__ uint32_t q_frag(const uint32_t (&q)[N]) {
@@ -178,7 +192,9 @@ __device__ __forceinline__ uint32_t q_frag(const uint32_t (&q)[N]) {
 
 // MT: query heads of a row of work (8: rows 8-15 of the MMA's A carry the low
 // halves of the weights; 16: a second MMA does)
-template <int D, int CT, int MT>
+// SPLIT: the shares described above; else a CTA does one row of work alone, with
+// the weights of its keys, and nothing is joined (see decode_direct)
+template <int D, int CT, int MT, bool SPLIT>
 __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a) {
   using Tile = DecTile<D, CT>;
   constexpr int kRow = Tile::kRow, S = Tile::kStages;
@@ -191,62 +207,81 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
   __shared__ long long s_sum[kDecWarps];
   __shared__ long long s_base, s_off;
   __shared__ int s_b;
-  __shared__ float s_m[kDecWarps][MT], s_l[kDecWarps][MT];
+  __shared__ float s_m[kDecWarps][MT], s_l[kDecWarps][MT], s_lse[MT];
   __shared__ uint8_t s_ok[kDecWarps][S];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int HG = a.c.H * a.GT;
   const int page_mask = (1 << a.c.page_log2) - 1;
-  pdl_launch();
-
-  // ---- this CTA's share of all blocks
-  long long mine = 0;
-  for (int b = tid; b < a.c.B; b += kDecThreads) {
-    const int n = cache_len(a.c, b);
-    if (blockIdx.x == 0 && a.c.lens[b] != n) record_page_error();
-    mine += visible_span(n, a.window, a.sinks).vb;
-  }
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, x);
-  if (lane == 0) s_sum[warp] = mine;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kDecWarps; ++w) total += s_sum[w];
-  total *= HG;
-  const long long share = max((long long)kMinShare, (total + gridDim.x - 1) / gridDim.x);
-  long long u = blockIdx.x * share;
-  const long long u_end = min(total, u + share);
-  if (blockIdx.x == 0 && tid == 0) a.prefix[a.c.B] = share;
-  if (u >= u_end && blockIdx.x != 0) return;
-  if (tid == 0) s_base = 0;
-  for (int b0 = 0; b0 < a.c.B; b0 += kDecThreads) {
-    const int b = b0 + tid;
-    const long long x =
-        b < a.c.B ? (long long)visible_span(cache_len(a.c, b), a.window, a.sinks).vb * HG : 0;
-    long long v = x;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, v, d);
-      if (lane >= d) v += y;
-    }
-    __syncthreads();
-    if (lane == 31) s_sum[warp] = v;
-    __syncthreads();
-    long long before = s_base + v - x;
-    for (int w = 0; w < warp; ++w) before += s_sum[w];
-    if (blockIdx.x == 0 && b < a.c.B) a.prefix[b] = before;
-    if (before <= u && u < before + x) {
-      s_b = b;
-      s_off = u - before;
-    }
-    __syncthreads();
-    if (tid == kDecThreads - 1) s_base = before + x;
-  }
-  __syncthreads();
-  if (u >= u_end) return;
-  int b = s_b;
-  long long off = s_off;
+  int b;
+  long long off, u, u_end;  // the share: blocks [u, u_end), the first one `off` blocks into sequence b
   bool first_piece = true;
+  if constexpr (SPLIT) {
+    pdl_launch();
+    // ---- this CTA's share of all blocks
+    long long mine = 0;
+    for (int seq = tid; seq < a.c.B; seq += kDecThreads) {
+      const int n = cache_len(a.c, seq);
+      if (blockIdx.x == 0 && a.c.lens[seq] != n) record_page_error();
+      mine += visible_span(n, a.window, a.sinks).vb;
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, x);
+    if (lane == 0) s_sum[warp] = mine;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) total += s_sum[w];
+    total *= HG;
+    const long long share = max((long long)kMinShare, (total + gridDim.x - 1) / gridDim.x);
+    u = blockIdx.x * share;
+    u_end = min(total, u + share);
+    if (blockIdx.x == 0 && tid == 0) a.prefix[a.c.B] = share;
+    if (u >= u_end && blockIdx.x != 0) return;
+    if (tid == 0) s_base = 0;
+    for (int b0 = 0; b0 < a.c.B; b0 += kDecThreads) {
+      const int seq = b0 + tid;
+      const long long x =
+          seq < a.c.B ? (long long)visible_span(cache_len(a.c, seq), a.window, a.sinks).vb * HG : 0;
+      long long v = x;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += y;
+      }
+      __syncthreads();
+      if (lane == 31) s_sum[warp] = v;
+      __syncthreads();
+      long long before = s_base + v - x;
+      for (int w = 0; w < warp; ++w) before += s_sum[w];
+      if (blockIdx.x == 0 && seq < a.c.B) a.prefix[seq] = before;
+      if (before <= u && u < before + x) {
+        s_b = seq;
+        s_off = u - before;
+      }
+      __syncthreads();
+      if (tid == kDecThreads - 1) s_base = before + x;
+    }
+    __syncthreads();
+    if (u >= u_end) return;
+    b = s_b;
+    off = s_off;
+  } else {
+    b = blockIdx.x / HG;
+    const int n = cache_len(a.c, b);
+    if (blockIdx.x % HG == 0 && tid == 0 && a.c.lens[b] != n) record_page_error();
+    u = 0;
+    u_end = visible_span(n, a.window, a.sinks).vb;
+    off = (blockIdx.x % HG) * u_end;
+    if (u_end == 0) {  // no key: o = 0
+      const int gt = blockIdx.x % a.GT, nh = min(MT, a.G - gt * MT);
+      const int hq0 = blockIdx.x % HG / a.GT * a.G + gt * MT;
+      for (int r = warp; r < nh; r += kDecWarps) {
+        for (int d = lane; d < D; d += 32) store16(a.o, ((int64_t)b * a.Hq + hq0 + r) * D + d, 0.0f, a.q_fp16);
+        write_lse<D>(a, b, hq0 + r, -INFINITY, 0.0f);
+      }
+      return;
+    }
+  }
 
   uint8_t* ring = smem + warp * Tile::kWarpBytes;
   const uint32_t ring_u = smem_u32(ring);
@@ -254,7 +289,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
 
   while (u < u_end) {
     const Span sp = visible_span(cache_len(a.c, b), a.window, a.sinks);
-    if (sp.vb == 0) {  // an empty sequence between two
+    if (SPLIT && sp.vb == 0) {  // an empty sequence between two
       ++b;
       continue;
     }
@@ -555,7 +590,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
       }
     }
     __syncthreads();
-    const bool whole = blk0 == 0 && nblk == sp.vb;
+    const bool whole = !SPLIT || (blk0 == 0 && nblk == sp.vb);
     const int slot = 2 * blockIdx.x + (first_piece ? 0 : 1);
     for (int r = warp; r < nh; r += kDecWarps) {
       float mm = -INFINITY;
@@ -579,12 +614,17 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
       }
       if (whole) {
         write_lse<D>(a, b, hq0 + r, mm, ll);
+        if (!SPLIT && lane == 0) s_lse[r] = ll > 0.0f || isnan(ll) ? mm + log2f(ll) : -INFINITY;
       } else if (lane == 0) {
         a.part_m[slot * kMaxGroup + r] = mm;
         a.part_l[slot * kMaxGroup + r] = ll;
       }
     }
     __syncthreads();  // the rings may be filled again
+    if (!SPLIT && a.scores && a.GT == 1) {  // (more tiles of a group share the weights: decode_weight_kernel)
+      for (int i = tid; i < sp.vb * kBlk; i += kDecThreads)
+        add_weight(a, sp, b, h, i, [&](int g) { return s_lse[g]; });
+    }
     u += nblk;
     off += nblk;
     first_piece = false;
@@ -658,50 +698,55 @@ __global__ void __launch_bounds__(128) decode_join_kernel(const DecodeArgs a) {
   if (tid < 32) write_lse<D>(a, b, hq, mx, l);
 }
 
-// weight[j] += sum over the group's heads of 2^(t_j - lse2); one thread a key
+// the weights of all keys, one thread a key
 __global__ void __launch_bounds__(256) decode_weight_kernel(const DecodeArgs a) {
   pdl_wait();
   const int b = blockIdx.x / a.c.H, h = blockIdx.x % a.c.H;
   const Span sp = visible_span(cache_len(a.c, b), a.window, a.sinks);
-  const int page = 1 << a.c.page_log2;
-  for (int64_t i = (int64_t)blockIdx.y * 256 + threadIdx.x; i < (int64_t)sp.vb * kBlk; i += (int64_t)gridDim.y * 256) {
-    const int j = span_block(sp, (int)(i / kBlk)) * kBlk + (int)(i % kBlk);
-    if (j >= sp.n || (j < sp.ws && j >= a.sinks)) continue;
-    const int pid = a.c.table[(int64_t)b * a.c.max_pages + (j >> a.c.page_log2)];
-    if (pid < 0 || pid >= a.c.n_pages) continue;
-    float x = 0.0f;
-    for (int g = 0; g < a.G; ++g) {
-      const int64_t row = (int64_t)b * a.Hq + h * a.G + g;
-      x += exp2f(a.scores[row * a.score_cap + i] - a.lse2[row]);
-    }
-    a.c.weight[((int64_t)pid * a.c.H + h) * page + (j & (page - 1))] += x;
-  }
+  const float* lse2 = a.lse2 + (int64_t)b * a.Hq + h * a.G;
+  for (int i = blockIdx.y * 256 + threadIdx.x; i < sp.vb * kBlk; i += gridDim.y * 256)
+    add_weight(a, sp, b, h, i, [&](int g) { return lse2[g]; });
 }
 
 template <int D, int CT, int MT>
 cudaError_t launch_decode_t(const DecodeArgs& a, cudaStream_t st) {
   constexpr int smem = kDecWarps * DecTile<D, CT>::kWarpBytes;
   static_assert(MT * D * 4 <= DecTile<D, CT>::kWarpBytes, "a warp's ring holds its rows of O for the merge");
-  auto kernel = decode_kernel<D, CT, MT>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int64_t want = (a.score_cap + 255) / 256;
+  const dim3 weights((unsigned)(a.c.B * a.c.H), (unsigned)(want < 64 ? want : 64));
+  cudaError_t e;
+  if (a.direct) {
+    auto kernel = decode_kernel<D, CT, MT, false>;
+    static DeviceOnce once;
+    e = once.run([&](int) { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)(a.c.B * a.c.H * a.GT), kDecThreads, smem, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess || !a.scores || a.GT == 1) return e;
+    decode_weight_kernel<<<weights, 256, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+  auto kernel = decode_kernel<D, CT, MT, true>;
+  static DeviceOnce once;
+  int wave = 0;  // CTAs that run at a time
+  e = once.run([&](int dev) {
+    int sms = 0, per = 0;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kDecThreads, smem);
+    once.value[dev] = sms * (per < 1 ? 1 : per);
+    return e;
+  }, &wave);
   if (e != cudaSuccess) return e;
-  int dev = 0, sms = 0, per = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kDecThreads, smem)) != cudaSuccess) return e;
   // one wave; no more CTAs than the smallest shares of the longest sequences
-  int64_t ctas = (int64_t)sms * (per < 1 ? 1 : per);
   const int64_t blocks = (int64_t)a.c.B * a.c.H * a.GT * ((a.c.cap + kBlk - 1) / kBlk);
-  if (ctas > (blocks + kMinShare - 1) / kMinShare) ctas = (blocks + kMinShare - 1) / kMinShare;
+  int64_t ctas = (blocks + kMinShare - 1) / kMinShare;
+  if (ctas > wave) ctas = wave;
   if (ctas > kDecodeCtas) ctas = kDecodeCtas;
-  if (ctas < 1) ctas = 1;
   kernel<<<(unsigned)ctas, kDecThreads, smem, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   e = launch_pdl(decode_join_kernel<D, MT>, dim3((unsigned)(a.c.B * a.Hq)), dim3(128), 0, st, a);
   if (e != cudaSuccess || !a.scores) return e;
-  const int64_t want = (a.score_cap + 255) / 256;
-  return launch_pdl(decode_weight_kernel, dim3((unsigned)(a.c.B * a.c.H), (unsigned)(want < 64 ? want : 64)), dim3(256),
-                    0, st, a);
+  return launch_pdl(decode_weight_kernel, weights, dim3(256), 0, st, a);
 }
 
 template <int D, int CT>

@@ -1,6 +1,7 @@
 // serving.cuh -- argument blocks and device helpers of the paged key-value
 // cache, the single-token attention over it and the sliding-window attention.
 #pragma once
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -47,6 +48,7 @@ struct DecodeArgs {
   int window, sinks;
   int q_fp16;
   float scale_log2, sm_scale;
+  int direct;  // a CTA a row of work, nothing to join (decode_direct)
   // workspace
   long long* prefix;  // [B] units before sequence b; [B] = units a CTA
   float* part_m;      // [2 kDecodeCtas][kMaxGroup]
@@ -76,6 +78,7 @@ struct WindowArgs {
   const int* lens;
   int B, Hq, Hkv, N, D;
   int nhd, window, sinks;
+  int zero_tail;  // rows behind a sequence's end: 1 zeros into o, 2 into lse
   float sm_scale, scale_log2;
   int items, pairs, group;  // set at launch: work items, row pairs of a head, heads whose items follow one another
 };
@@ -84,6 +87,29 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t st);
 cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t st);
 cudaError_t launch_attn_decode(const DecodeArgs& a, int quantized, cudaStream_t st);
 cudaError_t launch_attn_window(const WindowArgs& a, int is_fp16, cudaStream_t st);
+
+// ------------------------------------------------------------------ host
+// What a launcher asks of the current device once (attributes of a kernel, its
+// CTAs that run at a time): a call of microseconds has no time to ask again.
+// Two threads may both ask; they get the same answer.
+struct DeviceOnce {
+  static constexpr int kDevices = 64;
+  std::atomic<bool> done[kDevices] = {};
+  int value[kDevices] = {};  // what f(device) leaves there
+  template <typename F>
+  cudaError_t run(F&& f, int* got = nullptr) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= kDevices) return cudaErrorInvalidDevice;
+    if (!done[dev].load(std::memory_order_acquire)) {
+      if ((e = f(dev)) != cudaSuccess) return e;
+      done[dev].store(true, std::memory_order_release);
+    }
+    if (got) *got = value[dev];
+    return cudaSuccess;
+  }
+};
 
 // ------------------------------------------------------------------ cache
 __device__ __forceinline__ void record_page_error() { atomicExch(&g_page_error, 1u); }
@@ -106,6 +132,16 @@ __device__ __forceinline__ Span visible_span(int n, int window, int sinks) {
   s.vb = s.nsb + (n + kBlk - 1) / kBlk - s.wb;
   return s;
 }
+// blocks that a query can look at, at most (cap: slots of a sequence)
+inline int64_t most_blocks(int64_t cap, int window, int sinks) {
+  const int64_t all = (cap + kBlk - 1) / kBlk;
+  const int64_t seen = (int64_t)window / kBlk + 2 + ((int64_t)sinks + kBlk - 1) / kBlk;
+  return window > 0 && seen < all ? seen : all;
+}
+// Whether a row of work of at most `blocks` blocks goes to one CTA: short ones (a split's second kernel
+// costs more than the 8 turns of 4 warps), and those of up to four times the length when there are rows
+// enough for every SM twice.
+inline bool decode_direct(int64_t rows, int64_t blocks) { return blocks <= 32 || (blocks <= 128 && rows >= 296); }
 __device__ __forceinline__ int span_block(const Span& s, int i) { return i < s.nsb ? i : s.wb + i - s.nsb; }
 
 // ------------------------------------------------------------------ types

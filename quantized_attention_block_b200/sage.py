@@ -86,7 +86,8 @@ class SageDecodeParams(ctypes.Structure):
 class SageWindowParams(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("N", ctypes.c_int32),
                 ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("layout", ctypes.c_int32),
-                ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("sm_scale", ctypes.c_float)]
+                ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("sm_scale", ctypes.c_float),
+                ("zero_tail", ctypes.c_int32)]
 
 
 _lib = None
@@ -429,6 +430,8 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 def _expect(name: str, t: torch.Tensor, shape, dtype) -> None:
     """A contiguous tensor of this shape (None: any extent) and type, else ValueError."""
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
     if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
@@ -439,18 +442,15 @@ def _expect(name: str, t: torch.Tensor, shape, dtype) -> None:
         raise ValueError(f"{name} must be contiguous")
 
 
-def _one_device(**ts) -> torch.device:
-    """The CUDA device that all the tensors (None: absent) are on."""
-    device = None
-    for name, t in ts.items():
-        if t is None:
-            continue
-        device = t.device if device is None else device
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA device, got {device}")
-    return device
+def _one_device(names: str, *ts) -> int:
+    """The number of the CUDA device that all the tensors (None: absent) are on."""
+    index = ts[0].get_device()
+    for t in ts:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{names} must be on one device, got {[str(x.device) for x in ts if x is not None]}")
+    if index < 0 or ts[0].device.type != "cuda":
+        raise ValueError(f"{names} must be on a CUDA device, got {ts[0].device}")
+    return index
 
 
 def _layout(tensor_layout: str) -> int:
@@ -465,16 +465,35 @@ def _range32(**ns) -> None:
             raise ValueError(f"{name} must be in [0, 2^31), got {n}")
 
 
-def _raw_stream(stream, device) -> int:
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+class _On:
+    """Work on a device (by number) and a stream (None: the device's current one): `raw` for the library; tensors
+    made inside belong to both.  Switches to them only if they are not current: the smallest calls take less time
+    than torch's own guards."""
+
+    __slots__ = ("raw", "guards")
+
+    def __init__(self, index: int, stream: Optional[torch.cuda.Stream]):
+        self.guards = []
+        if index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(index))
+        if stream is None:
+            self.raw = torch.cuda.current_stream(index).cuda_stream if _raw_stream is None else _raw_stream(index)
+        else:
+            self.guards.append(torch.cuda.stream(stream))
+            self.raw = stream.cuda_stream
+
+    def __enter__(self) -> int:
+        for g in self.guards:
+            g.__enter__()
+        return self.raw
+
+    def __exit__(self, *exc) -> None:
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
 
 
-def _empty_on(stream, *specs):
-    """Tensors for work on `stream` (None: the current one), made so that the allocator knows it."""
-    if stream is None:
-        return [torch.empty(shape, dtype=dt, device=dev) for shape, dt, dev in specs]
-    with torch.cuda.stream(stream):
-        return [torch.empty(shape, dtype=dt, device=dev) for shape, dt, dev in specs]
+# torch's own handle of a device's current stream, without the Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 class KVCache:
@@ -511,6 +530,7 @@ class KVCache:
         self.k_pages, self.v_pages, self.k_scale, self.v_scale, self.weight = k_pages, v_pages, k_scale, v_scale, weight
         self.n_pages, self.Hkv, self.page_size, self.d, self.tensor_layout = n_pages, heads, page, d, tensor_layout
         self.device = k_pages.device
+        self._index = k_pages.get_device()
         for t in (v_pages, k_scale, v_scale, weight):
             if t is not None and t.device != self.device:
                 raise ValueError(f"the cache's tensors must be on one device, got {self.device} and {t.device}")
@@ -537,8 +557,10 @@ class KVCache:
         return self._c[dtype]
 
     def _seqs(self, page_table, lens) -> SageKvSeqs:
-        _expect("page_table", page_table, (None, None), torch.int32)
+        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+            _expect("page_table", page_table, (None, None), torch.int32)
         B, max_pages = page_table.shape
+        _expect("page_table", page_table, (B, max_pages), torch.int32)
         _expect("lens", lens, (B,), torch.int32)
         if B < 1 or max_pages < 1:
             raise ValueError(f"page_table must not be empty, got {tuple(page_table.shape)}")
@@ -563,10 +585,10 @@ def sage_kv_append(k, v, cache: KVCache, page_table, lens, *, n_new=None, km=Non
         if not cache.quantized:
             raise ValueError("km goes with a quantized cache")
         _expect("km", km, (s.B, cache.Hkv, cache.d), torch.float32)
-    device = _one_device(k=k, v=v, cache=cache.k_pages, page_table=page_table, lens=lens, n_new=n_new, km=km)
-    with torch.cuda.device(device):
+    index = _one_device("cache, k, v, page_table, lens, n_new, km", cache.k_pages, k, v, page_table, lens, n_new, km)
+    with _On(index, stream) as raw:
         _check(lib().sage_kv_append(k.data_ptr(), v.data_ptr(), _ptr(n_new), _ptr(km), T, layout, ctypes.byref(c),
-                                    ctypes.byref(s), _raw_stream(stream, device)), "sage_kv_append")
+                                    ctypes.byref(s), raw), "sage_kv_append")
 
 
 def decode_workspace_bytes(cache: KVCache, page_table, lens, Hq: int, *, window: int = 0, sinks: int = 0) -> int:
@@ -581,8 +603,8 @@ def decode_workspace_bytes(cache: KVCache, page_table, lens, Hq: int, *, window:
 def _decode(q, cache, page_table, lens, window, sinks, sm_scale, km, out, lse, want_lse, workspace, stream):
     _range32(window=window, sinks=sinks)
     c, s = cache._struct(q.dtype), cache._seqs(page_table, lens)
-    _expect("q", q, (s.B, None, cache.d), q.dtype)
-    Hq = q.shape[1]
+    Hq = q.shape[1] if q.dim() == 3 else 0
+    _expect("q", q, (s.B, Hq, cache.d), q.dtype)
     if Hq < 1 or Hq % cache.Hkv:
         raise ValueError(f"query heads must be a multiple of {cache.Hkv}, got {Hq}")
     if out is not None:
@@ -594,22 +616,21 @@ def _decode(q, cache, page_table, lens, window, sinks, sm_scale, km, out, lse, w
             raise ValueError("km goes with a quantized cache")
         _expect("km", km, (s.B, cache.Hkv, cache.d), torch.float32)
     if workspace is not None:
-        _expect("workspace", workspace, (None,), torch.uint8)
-    device = _one_device(q=q, cache=cache.k_pages, page_table=page_table, lens=lens, km=km, out=out, lse=lse,
-                         workspace=workspace)
+        _expect("workspace", workspace, (workspace.numel(),), torch.uint8)
+    index = _one_device("cache, q, page_table, lens, km, out, lse, workspace", cache.k_pages, q, page_table, lens, km,
+                        out, lse, workspace)
     p = SageDecodeParams(Hq, window, sinks, float(sm_scale if sm_scale else 0.0))
     L = lib()
-    with torch.cuda.device(device):
+    args = ctypes.byref(c), ctypes.byref(s), ctypes.byref(p)
+    with _On(index, stream) as raw:
         if out is None:
-            out, = _empty_on(stream, (q.shape, q.dtype, device))
+            out = torch.empty_like(q)
         if lse is None and want_lse:
-            lse, = _empty_on(stream, ((s.B, Hq), torch.float32, device))
+            lse = q.new_empty((s.B, Hq), dtype=torch.float32)
         if workspace is None:
-            n = L.sage_decode_workspace_bytes(ctypes.byref(c), ctypes.byref(s), ctypes.byref(p))
-            workspace, = _empty_on(stream, ((n,), torch.uint8, device))
-        _check(L.sage_attn_decode(q.data_ptr(), out.data_ptr(), _ptr(lse), _ptr(km), ctypes.byref(c), ctypes.byref(s),
-                                  ctypes.byref(p), workspace.data_ptr(), workspace.numel(),
-                                  _raw_stream(stream, device)), "sage_attn_decode")
+            workspace = q.new_empty((L.sage_decode_workspace_bytes(*args),), dtype=torch.uint8)
+        _check(L.sage_attn_decode(q.data_ptr(), out.data_ptr(), _ptr(lse), _ptr(km), *args, workspace.data_ptr(),
+                                  workspace.numel(), raw), "sage_attn_decode")
     return out, lse
 
 
@@ -642,23 +663,23 @@ def sage_kv_evict(cache: KVCache, page_table, lens, dst_table, keep: int, *, sin
     if keep < 1 or sinks + recent > keep:
         raise ValueError(f"keep must be at least 1 and hold sinks and recent, got {keep}, {sinks}, {recent}")
     c, s = next(iter(cache._c.values())), cache._seqs(page_table, lens)
-    _expect("dst_table", dst_table, (s.B, None), torch.int32)
+    n = dst_table.shape[1] if dst_table.dim() == 2 else 0
+    _expect("dst_table", dst_table, (s.B, n), torch.int32)
     if dst_table.shape[1] * cache.page_size < keep:
         raise ValueError(f"dst_table holds {dst_table.shape[1]} pages of {cache.page_size}: too few for {keep} tokens")
     if new_lens is not None:
         _expect("new_lens", new_lens, (s.B,), torch.int32)
     if kept is not None:
         _expect("kept", kept, (s.B, cache.Hkv, keep), torch.int32)
-    device = _one_device(cache=cache.k_pages, page_table=page_table, lens=lens, dst_table=dst_table,
-                         new_lens=new_lens, kept=kept)
-    with torch.cuda.device(device):
+    index = _one_device("cache, page_table, lens, dst_table, new_lens, kept", cache.k_pages, page_table, lens,
+                        dst_table, new_lens, kept)
+    with _On(index, stream) as raw:
         if new_lens is None:
-            new_lens, = _empty_on(stream, ((s.B,), torch.int32, device))
+            new_lens = torch.empty_like(lens)
         if kept is None:
-            kept, = _empty_on(stream, ((s.B, cache.Hkv, keep), torch.int32, device))
+            kept = lens.new_empty((s.B, cache.Hkv, keep))
         _check(lib().sage_kv_evict(ctypes.byref(c), ctypes.byref(s), dst_table.data_ptr(), dst_table.shape[1], keep,
-                                   sinks, recent, new_lens.data_ptr(), kept.data_ptr(),
-                                   _raw_stream(stream, device)), "sage_kv_evict")
+                                   sinks, recent, new_lens.data_ptr(), kept.data_ptr(), raw), "sage_kv_evict")
     return new_lens, kept
 
 
@@ -681,21 +702,16 @@ def _window_fwd(q, k, v, window, sinks, lens, sm_scale, out, lse, want_lse, stre
         _expect("out", out, q.shape, q.dtype)
     if lse is not None:
         _expect("lse", lse, (B, Hq, N), torch.float32)
-    device = _one_device(q=q, k=k, v=v, lens=lens, out=out, lse=lse)
-    p = SageWindowParams(B, Hq, Hkv, N, d, _DTYPES[q.dtype], layout, window, sinks, float(sm_scale if sm_scale else 0.0))
-    with torch.cuda.device(device):
-        made = []
+    index = _one_device("q, k, v, lens, out, lse", q, k, v, lens, out, lse)
+    # rows behind a sequence's end are not written: zeros in tensors made here
+    zero = 0 if lens is None else (1 if out is None else 0) | (2 if lse is None else 0)
+    p = SageWindowParams(B, Hq, Hkv, N, d, _DTYPES[q.dtype], layout, window, sinks, float(sm_scale if sm_scale else 0.0),
+                         zero)
+    with _On(index, stream) as raw:
         if out is None:
-            out, = _empty_on(stream, (q.shape, q.dtype, device))
-            made.append(out)
+            out = torch.empty_like(q)
         if lse is None and want_lse:
-            lse, = _empty_on(stream, ((B, Hq, N), torch.float32, device))
-            made.append(lse)
-        raw = _raw_stream(stream, device)
-        if lens is not None:  # rows behind a sequence's end are not written: zeros in tensors made here
-            with torch.cuda.stream(stream):
-                for t in made:
-                    t.zero_()
+            lse = q.new_empty((B, Hq, N), dtype=torch.float32)
         _check(lib().sage_attn_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse),
                                           _ptr(lens), ctypes.byref(p), raw), "sage_attn_window_fwd")
     return out, lse
