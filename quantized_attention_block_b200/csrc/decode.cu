@@ -54,6 +54,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool p
   const int n = pred ? 16 : 0;  // 0: fills with zeros, reads nothing
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -104,17 +107,15 @@ __device__ __forceinline__ void int8x4_to_half(uint32_t x, uint32_t& p01, uint32
   p23 = *reinterpret_cast<uint32_t*>(&b);
 }
 
-// the E4M3 codes in bytes (0, 2) and (1, 3) of a word -> bf16 pairs (exact):
-// the code's fields under bf16's exponent, times 2^120 (subnormals included)
-__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t x, uint32_t& even, uint32_t& odd) {
-  const uint32_t e = ((x << 8) & 0x80008000u) | ((x << 4) & 0x07F007F0u);
-  const uint32_t o = (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u);
-  const uint32_t k = 0x7B807B80u;  // 2^120
-  const __nv_bfloat162 kk = *reinterpret_cast<const __nv_bfloat162*>(&k);
-  __nv_bfloat162 a = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&e), kk);
-  __nv_bfloat162 b = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&o), kk);
-  even = *reinterpret_cast<uint32_t*>(&a);
-  odd = *reinterpret_cast<uint32_t*>(&b);
+// the E4M3 codes in bytes (0, 2) and (1, 3) of a word -> fp16 pairs (exact)
+__device__ __forceinline__ void e4m3x4_to_half(uint32_t x, uint32_t& even, uint32_t& odd) {
+  const uint32_t y = __byte_perm(x, x, 0x3120);
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(even), "=r"(odd)
+      : "r"(y));
 }
 
 // a pair of fp32 weights as 16-bit numbers, and what that rounding left over
@@ -202,13 +203,13 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
   constexpr int kChunks = kRow / 16;
   constexpr int kRowsPerLoad = 32 / kChunks;
   constexpr int NT = D / 8;                        // n-tiles of O
-  constexpr bool kVB = CT != kFP16;                // V and the weights as bf16
+  constexpr bool kVB = CT == kBF16;                // V and the weights as bf16
+  constexpr int E = CT == kQ8 ? 1 : 2;             // bytes of an element
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ long long s_sum[kDecWarps];
   __shared__ long long s_base, s_off;
   __shared__ int s_b;
   __shared__ float s_m[kDecWarps][MT], s_l[kDecWarps][MT], s_lse[MT];
-  __shared__ uint8_t s_ok[kDecWarps][S];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int HG = a.c.H * a.GT;
   const int page_mask = (1 << a.c.page_log2) - 1;
@@ -285,7 +286,13 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
 
   uint8_t* ring = smem + warp * Tile::kWarpBytes;
   const uint32_t ring_u = smem_u32(ring);
+  // this lane's 16 bytes of the rows of a load: offset in a page, place in the ring
   const int ld_row = lane / kChunks, ld_chunk = lane % kChunks;
+  const int row_bytes = (int)(a.c.rs * E);
+  const int64_t ld_off = ld_row * row_bytes + ld_chunk * 16;
+  // ldmatrix: row of K (rows of a matrix are keys), row of V (transposed); the chunk's number is XORed in
+  const uint32_t k_lane = swz<kRow>((lane / 16) * 8 + lane % 8, lane / 8 & 1);
+  const uint32_t v_lane = swz<kRow>((lane / 8 & 1) * 8 + lane % 8, lane / 16);
 
   while (u < u_end) {
     const Span sp = visible_span(cache_len(a.c, b), a.window, a.sinks);
@@ -349,6 +356,8 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    int v_exp = -100;
+    float v_unit = __uint_as_float((127 + 14 + 100) << 23);  // 2^(14 - v_exp)
 
     const int mine_n = nblk > warp ? (nblk - warp + kDecWarps - 1) / kDecWarps : 0;
     auto page_of = [&](int i) {  // page of the warp's i-th block (0 behind the last)
@@ -356,32 +365,55 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
       const int key = span_block(sp, blk0 + warp + i * kDecWarps) * kBlk;
       return __ldg(table + (key >> a.c.page_log2));
     };
+    const uint8_t* k_base = static_cast<const uint8_t*>(a.c.k) + h * a.c.hs * E + ld_off;
+    const uint8_t* v_base = static_cast<const uint8_t*>(a.c.v) + h * a.c.hs * E + ld_off;
+    // whether every key of a block is visible
+    auto whole_block = [&](int key) { return key + kBlk <= sp.n && (key >= sp.ws || key + kBlk <= a.sinks); };
+    uint32_t okay = 0;  // bit x: the page of the block loaded x loads ago is one
     auto load = [&](int i, int pid) {
+      okay <<= 1;
       if (i < mine_n) {
         const int key = span_block(sp, blk0 + warp + i * kDecWarps) * kBlk;
-        const bool ok = pid >= 0 && pid < a.c.n_pages;
+        const bool ok = (uint32_t)pid < (uint32_t)a.c.n_pages;
         if (!ok) {
           record_page_error();
           pid = 0;
         }
+        okay |= ok;
         const uint32_t dst = ring_u + (i % S) * Tile::kStage;
         const int off0 = key & page_mask;
-        const int64_t at = (int64_t)pid * a.c.page_stride + h * a.c.hs + (int64_t)off0 * a.c.rs;
-        constexpr int E = CT == kQ8 ? 1 : 2;
-        const uint8_t* kp = static_cast<const uint8_t*>(a.c.k) + at * E + ld_chunk * 16;
-        const uint8_t* vp = static_cast<const uint8_t*>(a.c.v) + at * E + ld_chunk * 16;
+        const int64_t at = (int64_t)pid * (a.c.page_stride * E) + (int64_t)off0 * row_bytes;
+        const uint8_t *kp = k_base + at, *vp = v_base + at;
+        const uint32_t kd = dst + swz<kRow>(ld_row, ld_chunk);
+        // (rows kRowsPerLoad x further down: the swizzle XORs the chunk with a function of the row)
+        auto place = [&](int x) { return kd + x * 512 ^ (swz<kRow>(x * kRowsPerLoad, 0) & (kRow - 1)); };
+        if (ok && whole_block(key)) {
+          if (row_bytes == kRow) {  // rows next to each other: constant offsets
 #pragma unroll
-        for (int x = 0; x < kLoads; ++x) {
-          const int r = x * kRowsPerLoad + ld_row, j = key + r;
-          const bool see = ok && j < sp.n && (j >= sp.ws || j < a.sinks);
-          cp_async16(dst + swz<kRow>(r, ld_chunk), kp + (int64_t)r * a.c.rs * E, see);
-          cp_async16(dst + Tile::kBlkBytes + swz<kRow>(r, ld_chunk), vp + (int64_t)r * a.c.rs * E, see);
+            for (int x = 0; x < kLoads; ++x) {
+              cp_async16(place(x), kp + x * 512);
+              cp_async16(place(x) + Tile::kBlkBytes, vp + x * 512);
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < kLoads; ++x) {
+              cp_async16(place(x), kp + (int64_t)(x * kRowsPerLoad) * row_bytes);
+              cp_async16(place(x) + Tile::kBlkBytes, vp + (int64_t)(x * kRowsPerLoad) * row_bytes);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < kLoads; ++x) {
+            const int j = key + x * kRowsPerLoad + ld_row;
+            const bool see = ok && j < sp.n && (j >= sp.ws || j < a.sinks);
+            cp_async16(place(x), kp + (int64_t)(x * kRowsPerLoad) * row_bytes, see);
+            cp_async16(place(x) + Tile::kBlkBytes, vp + (int64_t)(x * kRowsPerLoad) * row_bytes, see);
+          }
         }
         if (CT == kQ8 && lane < 8) {
           const float* sc = (lane < 4 ? a.c.ks : a.c.vs) + ((int64_t)pid * a.c.H + h) * (page_mask + 1) + off0;
           cp_async16(dst + 2 * Tile::kBlkBytes + lane * 16, sc + (lane & 3) * 4, ok);
         }
-        if (lane == 0) s_ok[warp][i % S] = ok;
       }
       cp_commit();
     };
@@ -405,16 +437,16 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
       const float* sc = reinterpret_cast<const float*>(ring + (it % S) * Tile::kStage + 2 * Tile::kBlkBytes);
       const int ord = blk0 + warp + it * kDecWarps;
       const int key = span_block(sp, ord) * kBlk;
-      const bool ok = s_ok[warp][it % S];
+      const bool ok = okay >> (S - 1) & 1;
+      const bool whole = ok && whole_block(key);  // else some keys are masked
 
       // ---- S = Q K^T: two n-tiles of 8 keys
       float s[2][4] = {};
-      const int mi = lane / 8, mr = lane % 8;
       if constexpr (CT != kQ8) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           uint32_t r[4];
-          ldsm4(r, kt + swz<kRow>((mi >> 1) * 8 + mr, 2 * k + (mi & 1)));
+          ldsm4(r, (kt + k_lane) ^ (32 * k));
           const uint32_t a1 = q_frag<MT, 1>(qa[k]), a2 = q_frag<MT, 2>(qa[k]), a3 = q_frag<MT, 3>(qa[k]);
           mma16816<CT == kBF16>(s[0], qa[k][0], a1, a2, a3, r[0], r[1]);
           mma16816<CT == kBF16>(s[1], qa[k][0], a1, a2, a3, r[2], r[3]);
@@ -423,7 +455,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
 #pragma unroll
         for (int k = 0; k < D / 16; k += 2) {
           uint32_t r[4];
-          ldsm4(r, kt + swz<kRow>((mi >> 1) * 8 + mr, k + (mi & 1)));
+          ldsm4(r, (kt + k_lane) ^ (16 * k));
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const uint32_t a1 = q_frag<MT, 1>(qa[k + x]), a2 = q_frag<MT, 2>(qa[k + x]), a3 = q_frag<MT, 3>(qa[k + x]);
@@ -435,27 +467,59 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
           }
         }
       }
-      // ---- scale, mask, online softmax; s[t][c]: head lane / 4 (+ 8), key 8 t + 2 (lane % 4) + (c & 1)
-      bool see[2][2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int j = key + 8 * t + 2 * (lane & 3) + c;
-          see[t][c] = ok && j < sp.n && (j >= sp.ws || j < a.sinks);
-        }
+      // ---- scale, mask; s[t][c]: head lane / 4 (+ 8), key 8 t + 2 (lane % 4) + (c & 1)
       float vs[2][2];
       if constexpr (CT == kQ8) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const float2 ks = *reinterpret_cast<const float2*>(sc + 8 * t + 2 * (lane & 3));
           const float2 v2 = *reinterpret_cast<const float2*>(sc + 16 + 8 * t + 2 * (lane & 3));
-          vs[t][0] = see[t][0] ? v2.x : 0.0f;
-          vs[t][1] = see[t][1] ? v2.y : 0.0f;
+          vs[t][0] = v2.x;
+          vs[t][1] = v2.y;
 #pragma unroll
           for (int c = 0; c < 4; ++c) s[t][c] *= (c & 1) ? ks.y : ks.x;
         }
       }
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int c = 0; c < MT / 4; ++c) s[t][c] *= qs[c >> 1];
+      if (!whole) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int j = key + 8 * t + 2 * (lane & 3) + c;
+            if (!(ok && j < sp.n && (j >= sp.ws || j < a.sinks))) {
+              s[t][c] = s[t][2 + c] = -INFINITY;
+              if (CT == kQ8) vs[t][c] = 0.0f;
+            }
+          }
+      }
+      if constexpr (CT == kQ8) {
+        // the weights times V's scales are held as fp16 in units of 2^(v_exp - 14), v_exp above every scale so far
+        const float top = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));
+        if (__any_sync(0xffffffffu, top * v_unit >= 16384.0f)) {
+          float x = top;
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+          const int e = (int)(__float_as_uint(x) >> 23) - 126;  // x < 2^e (x is above 2^-101)
+          if (e <= 128) {
+            const float down = __uint_as_float((uint32_t)max(127 + v_exp - e, 0) << 23);
+            v_exp = e;
+            v_unit = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) o[n][c] *= down;
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) vs[t][c] *= v_unit;
+      }
+      // ---- online softmax
       float p[2][4];
 #pragma unroll
       for (int half = 0; half < MT / 8; ++half) {
@@ -464,9 +528,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float& x = s[t][2 * half + c];
-            x = see[t][c] ? x * qs[half] : -INFINITY;
-            mx = fmaxf(mx, x);
+            mx = fmaxf(mx, s[t][2 * half + c]);
           }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -512,8 +574,8 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
         for (int t = 0; t < 2; ++t) {
           float x = p[t][2 * half], y = p[t][2 * half + 1];
           if constexpr (CT == kQ8) {
-            x = see[t][0] ? x * vs[t][0] : 0.0f;
-            y = see[t][1] ? y * vs[t][1] : 0.0f;
+            x *= vs[t][0];
+            y *= vs[t][1];
           }
           split_pair<kVB>(x, y, hi[2 * t + half], lo[2 * t + half]);
         }
@@ -525,7 +587,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
 #pragma unroll
         for (int n = 0; n < NT; n += 2) {
           uint32_t r[4];
-          ldsm4t(r, vt + swz<kRow>((mi & 1) * 8 + mr, n + (mi >> 1)));
+          ldsm4t(r, (vt + v_lane) ^ (16 * n));
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             mma16816<kVB>(o[n + x], hi[0], hi[1], hi[2], hi[3], r[2 * x], r[2 * x + 1]);
@@ -539,12 +601,12 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
 #pragma unroll
         for (int c = 0; c < NT / 2; c += 2) {
           uint32_t r[4];
-          ldsm4t(r, vt + swz<kRow>((mi & 1) * 8 + mr, c + (mi >> 1)));
+          ldsm4t(r, (vt + v_lane) ^ (16 * c));
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             uint32_t e0, o0, e1, o1;
-            e4m3x4_to_bf16(r[2 * x], e0, o0);
-            e4m3x4_to_bf16(r[2 * x + 1], e1, o1);
+            e4m3x4_to_half(r[2 * x], e0, o0);
+            e4m3x4_to_half(r[2 * x + 1], e1, o1);
             float(&oe)[4] = o[2 * (c + x)];
             float(&oo)[4] = o[2 * (c + x) + 1];
             mma16816<kVB>(oe, hi[0], hi[1], hi[2], hi[3], e0, e1);
@@ -556,7 +618,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
           }
         }
       }
-      __syncwarp();  // the ring slot may be filled again, s_ok rewritten
+      __syncwarp();  // the ring slot may be filled again
     }
     cp_wait<0>();
     __syncthreads();  // every warp is done with its ring: the merge uses it
@@ -580,6 +642,10 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
           x0 += o[n][2];
           x1 += o[n][3];
         }
+        if constexpr (CT == kQ8) {
+          x0 *= __uint_as_float((uint32_t)(127 - 14 + v_exp) << 23);
+          x1 *= __uint_as_float((uint32_t)(127 - 14 + v_exp) << 23);
+        }
         if constexpr (CT != kQ8) {
           so[r * D + n * 8 + 2 * (lane & 3)] = x0;
           so[r * D + n * 8 + 2 * (lane & 3) + 1] = x1;
@@ -590,7 +656,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
       }
     }
     __syncthreads();
-    const bool whole = !SPLIT || (blk0 == 0 && nblk == sp.vb);
+    const bool alone = !SPLIT || (blk0 == 0 && nblk == sp.vb);
     const int slot = 2 * blockIdx.x + (first_piece ? 0 : 1);
     for (int r = warp; r < nh; r += kDecWarps) {
       float mm = -INFINITY;
@@ -603,16 +669,16 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
         f[w] = exp2f(s_m[w][r] - ms);
         ll += s_l[w][r] * f[w];
       }
-      const float inv = whole ? (ll > 0.0f || isnan(ll) ? 1.0f / ll : 0.0f) : 1.0f;
+      const float inv = alone ? (ll > 0.0f || isnan(ll) ? 1.0f / ll : 0.0f) : 1.0f;
       for (int d = lane; d < D; d += 32) {
         float x = 0.0f;
 #pragma unroll
         for (int w = 0; w < kDecWarps; ++w)
           x += reinterpret_cast<const float*>(smem + w * Tile::kWarpBytes)[r * D + d] * f[w];
-        if (whole) store16(a.o, ((int64_t)b * a.Hq + hq0 + r) * D + d, x * inv, a.q_fp16);
+        if (alone) store16(a.o, ((int64_t)b * a.Hq + hq0 + r) * D + d, x * inv, a.q_fp16);
         else a.part_o[((int64_t)slot * kMaxGroup + r) * D + d] = x;
       }
-      if (whole) {
+      if (alone) {
         write_lse<D>(a, b, hq0 + r, mm, ll);
         if (!SPLIT && lane == 0) s_lse[r] = ll > 0.0f || isnan(ll) ? mm + log2f(ll) : -INFINITY;
       } else if (lane == 0) {
