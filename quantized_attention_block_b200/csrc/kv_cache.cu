@@ -11,99 +11,118 @@ namespace sage {
 namespace {
 
 // ------------------------------------------------------------------ append
-// One row (token, head) of K or V is D / 8 lanes of 16 bytes.  Rows are taken
-// in the order of the input, so reads are contiguous; a row lands contiguous in
-// its page.  Bound: HBM (each token read and written once).
+// A row (token, head) of K and of V is D / 8 lanes of 16 bytes each.  Rows are
+// taken in the order of the input, so reads are contiguous; a row lands
+// contiguous in its page.  Bound: HBM (each token read and written once), so a
+// thread holds its 16 bytes of K and V of ROWS rows at a time: the loads of
+// ROWS = 4 are 128 bytes in flight a thread (prompts of 18k tokens of 8 heads of
+// 128: 66 us with one row of K or V a thread).  Few rows take ROWS = 1, to be
+// spread over more SMs.
 constexpr int kAppendThreads = 256;
 
-template <int D, bool QUANT, bool FP16>
+template <int D, bool QUANT, bool FP16, int ROWS>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a) {
-  constexpr int L = D / 8;  // lanes a row
-  const int64_t rows = (int64_t)a.c.B * a.T * a.c.H;
-  const int lane = threadIdx.x % L;
-  const int64_t row = ((int64_t)blockIdx.x * kAppendThreads + threadIdx.x) / L;
-  const bool is_v = blockIdx.y != 0;
-  const int page = 1 << a.c.page_log2;
-  // (b, h, t) of the row; the lanes of a row agree, so shuffles below are among active lanes
-  bool live = row < rows;
-  const int64_t r = live ? row : 0;
-  const int inner = (int)(r % (a.nhd ? a.c.H : a.T));
-  const int64_t outer = r / (a.nhd ? a.c.H : a.T);
-  const int mid = (int)(outer % (a.nhd ? a.T : a.c.H));
-  const int b = (int)(outer / (a.nhd ? a.T : a.c.H));
-  const int h = a.nhd ? inner : mid, t = a.nhd ? mid : inner;
-  const int n_new = a.n_new ? min(max(a.n_new[b], 0), a.T) : a.T;
-  live = live && t < n_new;
-  int pos = 0, pid = 0;
-  if (live) {
-    const int64_t p = (int64_t)cache_len(a.c, b) + t;
-    if (p >= a.c.cap || a.c.lens[b] < 0 || a.c.lens[b] > a.c.cap) record_page_error();
-    live = p < a.c.cap;
-    pos = (int)p;
+  constexpr int L = D / 8, PASS = kAppendThreads / L;  // lanes a row; rows of the CTA at a time
+  const int lane = threadIdx.x % L, b = blockIdx.y;
+  const uint32_t rows = (uint32_t)a.T * a.c.H, inner = a.nhd ? a.c.H : a.T;
+  const int n_new = a.n_new ? min(max(__ldg(a.n_new + b), 0), a.T) : a.T;
+  const int held = cache_len(a.c, b), page = 1 << a.c.page_log2;
+  if (n_new > 0 && blockIdx.x == 0 && threadIdx.x == 0 &&
+      (a.c.lens[b] != held || (int64_t)held + n_new > a.c.cap))
+    record_page_error();
+  // this thread's rows: (h, t), whether they are written (the lanes of a row agree, so shuffles below are among
+  // active lanes), their place
+  bool live[ROWS];
+  int h[ROWS], off[ROWS], pid[ROWS];
+  uint4 x[ROWS][2];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const uint32_t r = blockIdx.x * (ROWS * PASS) + i * PASS + threadIdx.x / L;
+    const uint32_t q = r / inner, m = r - q * inner;
+    const int t = a.nhd ? q : m;
+    h[i] = a.nhd ? m : q;
+    live[i] = r < rows && t < n_new && (uint32_t)held + (uint32_t)t < (uint32_t)a.c.cap;
+    pid[i] = off[i] = 0;
+    x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+    if (live[i]) {
+      const int64_t at = ((int64_t)b * rows + r) * L + lane;
+      x[i][0] = __ldcs(static_cast<const uint4*>(a.k) + at);
+      x[i][1] = __ldcs(static_cast<const uint4*>(a.v) + at);
+      pid[i] = __ldg(a.c.table + (int64_t)b * a.c.max_pages + ((held + t) >> a.c.page_log2));
+      off[i] = (held + t) & (page - 1);
+    }
   }
-  if (live) {
-    pid = a.c.table[(int64_t)b * a.c.max_pages + (pos >> a.c.page_log2)];
-    if (pid < 0 || pid >= a.c.n_pages) {
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    if (live[i] && (uint32_t)pid[i] >= (uint32_t)a.c.n_pages) {
       record_page_error();
-      live = false;
+      live[i] = false;
     }
-  }
-  uint4 x = make_uint4(0, 0, 0, 0);
-  if (live) x = reinterpret_cast<const uint4*>(is_v ? a.v : a.k)[r * L + lane];
-  const int off = pos & (page - 1);
-  const int64_t at = (int64_t)pid * a.c.page_stride + h * a.c.hs + off * a.c.rs + lane * 8;
-  const int64_t sat = ((int64_t)pid * a.c.H + h) * page + off;
-  if (live && lane == 0 && !is_v && a.c.weight) a.c.weight[sat] = 0.0f;
-  if constexpr (!QUANT) {
-    if (live) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? a.c.v : a.c.k) + at) = x;
-  } else {
-    using T = std::conditional_t<FP16, __half, __nv_bfloat16>;
-    float f[8];
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    const int64_t at = (int64_t)pid[i] * a.c.page_stride + h[i] * a.c.hs + off[i] * a.c.rs + lane * 8;
+    const int64_t sat = ((int64_t)pid[i] * a.c.H + h[i]) * page + off[i];
+    if (live[i] && lane == 0 && a.c.weight) a.c.weight[sat] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 p = unpack2<T>(w[i]);
-      f[2 * i] = p.x;
-      f[2 * i + 1] = p.y;
-    }
-    if (!is_v && a.km) {
-      const float* km = a.km + ((int64_t)b * a.c.H + h) * D + lane * 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = __fsub_rn(f[i], km[i]);
-    }
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(f[i]));
-#pragma unroll
-    for (int m = L / 2; m > 0; m >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-    const float s = __fdiv_rn(amax, is_v ? 448.0f : 127.0f);
-    uint32_t lo = 0, hi = 0;
-    if (s != 0.0f) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = __fdiv_rn(f[i], s);
-      if (is_v) {
-        lo = cvt_e4m3x4(f[0], f[1], f[2], f[3]);
-        hi = cvt_e4m3x4(f[4], f[5], f[6], f[7]);
+    for (int is_v = 0; is_v < 2; ++is_v) {
+      if constexpr (!QUANT) {
+        if (live[i]) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? a.c.v : a.c.k) + at) = x[i][is_v];
       } else {
+        using T = std::conditional_t<FP16, __half, __nv_bfloat16>;
+        float f[8];
+        const uint32_t w[4] = {x[i][is_v].x, x[i][is_v].y, x[i][is_v].z, x[i][is_v].w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = min(max(__float2int_rn(f[i]), -127), 127);
-          (i < 4 ? lo : hi) |= (uint32_t)(c & 255) << (8 * (i & 3));
+        for (int e = 0; e < 4; ++e) {
+          const float2 p = unpack2<T>(w[e]);
+          f[2 * e] = p.x;
+          f[2 * e + 1] = p.y;
+        }
+        if (!is_v && a.km && live[i]) {
+          const float4* km = reinterpret_cast<const float4*>(a.km + ((int64_t)b * a.c.H + h[i]) * D + lane * 8);
+          const float4 m0 = __ldg(km), m1 = __ldg(km + 1);
+          const float m[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = __fsub_rn(f[e], m[e]);
+        }
+        float amax = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = max_nan(amax, fabsf(f[e]));
+#pragma unroll
+        for (int m = L / 2; m > 0; m >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+        const float s = __fdiv_rn(amax, is_v ? 448.0f : 127.0f);
+        uint32_t lo = 0, hi = 0;
+        if (s != 0.0f) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = __fdiv_rn(f[e], s);
+          if (is_v) {
+            lo = cvt_e4m3x4(f[0], f[1], f[2], f[3]);
+            hi = cvt_e4m3x4(f[4], f[5], f[6], f[7]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int c = min(max(__float2int_rn(f[e]), -127), 127);
+              (e < 4 ? lo : hi) |= (uint32_t)(c & 255) << (8 * (e & 3));
+            }
+          }
+        }
+        if (live[i]) {
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? a.c.v : a.c.k) + at) = make_uint2(lo, hi);
+          if (lane == 0) (is_v ? a.c.vs : a.c.ks)[sat] = s;
         }
       }
-    }
-    if (live) {
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? a.c.v : a.c.k) + at) = make_uint2(lo, hi);
-      if (lane == 0) (is_v ? a.c.vs : a.c.ks)[sat] = s;
     }
   }
 }
 
 // ------------------------------------------------------------------ evict
 // Selection: one CTA per (b, kv head).  The weights' order-preserving bit
-// patterns are searched for the (keep - sinks - recent)-th largest, 8 bits a
-// pass; a last pass in token order counts what stays and writes its positions.
-constexpr int kSelThreads = 1024;
+// patterns are searched for the (keep - sinks - recent)-th largest, 11 bits a
+// pass (the first digit, sign, exponent and two bits, spreads weights over more
+// than a handful of counters); a last pass in token order counts what stays and
+// writes its positions.  The first pass keeps the patterns in shared memory
+// (those of the first kSelKeys tokens; the others are looked up again): a pass
+// through the page table took 30 us at 32k tokens, one over shared memory 3.
+constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
+constexpr int kSelBins = 2048;
+constexpr int kSelKeys = 53248;  // 208 KB
 
 // unsigned key in the order of the weights: NaN lowest, -0 as +0
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -113,7 +132,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 __device__ __forceinline__ uint32_t token_key(const CacheArgs& c, int b, int h, int j) {
-  const int pid = c.table[(int64_t)b * c.max_pages + (j >> c.page_log2)];
+  const int pid = __ldg(c.table + (int64_t)b * c.max_pages + (j >> c.page_log2));
   if (pid < 0 || pid >= c.n_pages) {
     record_page_error();
     return 0u;
@@ -149,11 +168,14 @@ __device__ __forceinline__ int block_scan(int x, int* s_warp, int* total) {
 }
 
 __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const EvictArgs a) {
-  __shared__ int s_hist[256];
-  __shared__ int s_warp[32];
+  extern __shared__ __align__(16) uint32_t s_keys[];  // candidates [0, min(hi - lo, held))
+  __shared__ int s_hist[kSelBins];
+  __shared__ int s_warp[32], s_tie[kSelWarps], s_stay[kSelWarps];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
+  pdl_launch();
   const int b = blockIdx.x / a.c.H, h = blockIdx.x % a.c.H, tid = threadIdx.x;
+  const int lane = tid & 31, warp = tid >> 5;
   const int n = cache_len(a.c, b);
   if (h == 0 && tid == 0) {
     if (a.c.lens[b] != n) record_page_error();
@@ -164,118 +186,191 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const EvictArgs 
     for (int i = tid; i < a.keep; i += kSelThreads) kept[i] = i < n ? i : -1;
     return;
   }
-  const int lo = a.sinks, hi = n - a.recent;  // candidates [lo, hi)
-  const int need = a.keep - a.sinks - a.recent;
+  const int lo = a.sinks, cand = n - a.recent - lo;  // candidates: tokens lo + [0, cand)
+  const int need = a.keep - a.sinks - a.recent;      // of them stay
+  const int held = min(cand, a.held_keys);
+  auto key_of = [&](int i) { return i < held ? s_keys[i] : token_key(a.c, b, h, lo + i); };
   uint32_t prefix = 0;
   int left = need;  // how many of the keys that match the prefix so far stay
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) s_hist[tid] = 0;
+  for (int pass = 0; pass < 3 && need > 0; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kSelBins;
+    for (int i = tid; i < bins; i += kSelThreads) s_hist[i] = 0;
     __syncthreads();
-    for (int j = lo + tid; j < hi; j += kSelThreads) {
-      const uint32_t key = token_key(a.c, b, h, j);
-      if (shift == 24 || (key >> (shift + 8)) == prefix) atomicAdd(&s_hist[(key >> shift) & 255], 1);
-    }
-    __syncthreads();
-    int total;
-    const int x = tid < 256 ? s_hist[255 - tid] : 0;  // from the largest digit down
-    const int before = block_scan(x, s_warp, &total);
-    if (tid < 256 && before < left && left <= before + x) {
-      s_prefix = (prefix << 8) | (255 - tid);
-      s_need = left - before;
-    }
-    __syncthreads();
-    if (left > 0) {
-      prefix = s_prefix;
-      left = s_need;
-    }
-    __syncthreads();
-  }
-  // `left` of the keys equal to `prefix` stay (the earliest); need == 0: none at all
-  int out = 0, ties = 0;
-  for (int j0 = 0; j0 < n; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    bool stay = false, tie = false;
-    if (j < n) {
-      if (j < lo || j >= hi) {
-        stay = true;
-      } else if (need > 0) {
-        const uint32_t key = token_key(a.c, b, h, j);
-        stay = key > prefix;
-        tie = key == prefix;
+    if (pass == 0) {
+      for (int i0 = tid; i0 < cand; i0 += 4 * kSelThreads) {
+        uint32_t k[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int i = i0 + x * kSelThreads;
+          if (i < cand) k[x] = token_key(a.c, b, h, lo + i);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int i = i0 + x * kSelThreads;
+          if (i < held) s_keys[i] = k[x];
+          if (i < cand) atomicAdd(&s_hist[k[x] >> 21], 1);
+        }
+      }
+    } else {
+      for (int i = tid; i < cand; i += kSelThreads) {
+        const uint32_t k = key_of(i);
+        if (k >> (pass == 1 ? 21 : 10) == prefix) atomicAdd(&s_hist[(k >> shift) & (bins - 1)], 1);
       }
     }
+    __syncthreads();
+    // the digit at which the count from the largest down reaches `left`; two bins a thread
+    const int i1 = bins - 1 - 2 * tid, i0 = i1 - 1;
+    const int x1 = i0 >= 0 ? s_hist[i1] : 0, x0 = i0 >= 0 ? s_hist[i0] : 0;
     int total;
-    const int tie_rank = ties + block_scan(tie ? 1 : 0, s_warp, &total);
-    ties += total;
-    stay = stay || (tie && tie_rank < left);
-    const int at = out + block_scan(stay ? 1 : 0, s_warp, &total);
-    out += total;
-    if (stay && at < a.keep) kept[at] = j;
+    const int before = block_scan(x1 + x0, s_warp, &total);
+    if (before < left && left <= before + x1 + x0) {
+      const bool first = left <= before + x1;
+      s_prefix = (prefix << (pass == 2 ? 10 : 11)) | (first ? i1 : i0);
+      s_need = left - before - (first ? 0 : x1);
+    }
+    __syncthreads();
+    prefix = s_prefix;
+    left = s_need;
+    __syncthreads();
   }
+  // `left` of the keys equal to `prefix` stay, the earliest.  A warp takes a run of tokens, 32 at a time: it counts
+  // the larger and the equal ones, then, with the counts of the warps before it, writes the positions.
+  const int run = ((cand + kSelThreads - 1) / kSelThreads) * 32;
+  const int i0 = warp * run, i1 = min(cand, i0 + run);
+  int more = 0, same = 0;
+  if (need > 0)
+    for (int i = i0; i < i1; i += 32) {
+      const uint32_t k = i + lane < i1 ? key_of(i + lane) : 0u;
+      more += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && k > prefix));
+      same += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && k == prefix));
+    }
+  if (lane == 0) {
+    s_stay[warp] = more;
+    s_tie[warp] = same;
+  }
+  __syncthreads();
+  int out = a.sinks, ties = 0;
+  for (int w = 0; w < warp; ++w) {
+    out += s_stay[w] + max(0, min(s_tie[w], left - ties));
+    ties += s_tie[w];
+  }
+  if (need > 0)
+    for (int i = i0; i < i1; i += 32) {
+      const uint32_t k = i + lane < i1 ? key_of(i + lane) : 0u;
+      const uint32_t tie = __ballot_sync(0xffffffffu, i + lane < i1 && k == prefix);
+      const uint32_t below = (1u << lane) - 1u;
+      const bool stay = i + lane < i1 && (k > prefix || (k == prefix && ties + __popc(tie & below) < left));
+      const uint32_t all = __ballot_sync(0xffffffffu, stay);
+      if (stay) kept[out + __popc(all & below)] = lo + i + lane;
+      out += __popc(all);
+      ties += __popc(tie);
+    }
+  for (int i = tid; i < a.sinks; i += kSelThreads) kept[i] = i;
+  for (int i = tid; i < a.recent; i += kSelThreads) kept[a.keep - a.recent + i] = n - a.recent + i;
 }
 
-// Moves the rows that stay.  One row of K or V is D * bytes / 16 lanes.
-constexpr int kMoveThreads = 256;
+// Moves the rows that stay.  One row of K or V is ROW_BYTES / 16 lanes; a thread
+// has its 16 bytes of K and V of four rows in flight.
+constexpr int kMoveThreads = 256, kMoveRows = 4;
 
 template <int ROW_BYTES>
 __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictArgs a) {
   pdl_wait();
   constexpr int L = ROW_BYTES / 16;
-  constexpr int RPC = kMoveThreads / L;  // rows a CTA pass
+  constexpr int PASS = kMoveThreads / L;  // rows of the CTA at a time
   const int bh = blockIdx.x, b = bh / a.c.H, h = bh % a.c.H;
   const int n = min(cache_len(a.c, b), a.keep);
   const int lane = threadIdx.x % L;
   const int page = 1 << a.c.page_log2;
   const int esize = a.quantized ? 1 : 2;
-  for (int i = blockIdx.y * RPC + threadIdx.x / L; i < n; i += gridDim.y * RPC) {
-    const int j = a.kept[(int64_t)bh * a.keep + i];
-    const int sp = a.c.table[(int64_t)b * a.c.max_pages + (j >> a.c.page_log2)];
-    const int dp = a.dst_table[(int64_t)b * a.dst_pages + (i >> a.c.page_log2)];
-    if (sp < 0 || sp >= a.c.n_pages || dp < 0 || dp >= a.c.n_pages) {
-      record_page_error();
-      continue;
+  for (int i0 = blockIdx.y * (PASS * kMoveRows) + threadIdx.x / L; i0 < n; i0 += gridDim.y * (PASS * kMoveRows)) {
+    int j[kMoveRows], sp[kMoveRows], dp[kMoveRows];
+    uint4 kx[kMoveRows], vx[kMoveRows];
+    float f[kMoveRows];  // lane 0: weight, 1 and 2: scales
+#pragma unroll
+    for (int x = 0; x < kMoveRows; ++x) {
+      const int i = i0 + x * PASS;
+      j[x] = i < n ? __ldg(a.kept + (int64_t)bh * a.keep + i) : -1;
+      dp[x] = i < n ? __ldg(a.dst_table + (int64_t)b * a.dst_pages + (i >> a.c.page_log2)) : 0;
     }
-    const int so = j & (page - 1), to = i & (page - 1);
-    const int64_t src = ((int64_t)sp * a.c.page_stride + h * a.c.hs + so * a.c.rs) * esize + lane * 16;
-    const int64_t dst = ((int64_t)dp * a.c.page_stride + h * a.c.hs + to * a.c.rs) * esize + lane * 16;
-    const uint4 kx = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.c.k) + src);
-    const uint4 vx = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.c.v) + src);
-    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.c.k) + dst) = kx;
-    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.c.v) + dst) = vx;
-    const int64_t ss = ((int64_t)sp * a.c.H + h) * page + so, ds = ((int64_t)dp * a.c.H + h) * page + to;
-    if (lane == 0) a.c.weight[ds] = a.c.weight[ss];
-    if (a.quantized && lane == 1) a.c.ks[ds] = a.c.ks[ss];
-    if (a.quantized && lane == 2) a.c.vs[ds] = a.c.vs[ss];
+#pragma unroll
+    for (int x = 0; x < kMoveRows; ++x)
+      sp[x] = j[x] >= 0 ? __ldg(a.c.table + (int64_t)b * a.c.max_pages + (j[x] >> a.c.page_log2)) : 0;
+#pragma unroll
+    for (int x = 0; x < kMoveRows; ++x) {
+      if (j[x] < 0) continue;
+      if ((uint32_t)sp[x] >= (uint32_t)a.c.n_pages || (uint32_t)dp[x] >= (uint32_t)a.c.n_pages) {
+        record_page_error();
+        j[x] = -1;
+        continue;
+      }
+      const int so = j[x] & (page - 1);
+      const int64_t src = ((int64_t)sp[x] * a.c.page_stride + h * a.c.hs + so * a.c.rs) * esize + lane * 16;
+      const int64_t ss = ((int64_t)sp[x] * a.c.H + h) * page + so;
+      kx[x] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.c.k) + src);
+      vx[x] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.c.v) + src);
+      if (lane == 0) f[x] = a.c.weight[ss];
+      if (a.quantized && lane == 1) f[x] = a.c.ks[ss];
+      if (a.quantized && lane == 2) f[x] = a.c.vs[ss];
+    }
+#pragma unroll
+    for (int x = 0; x < kMoveRows; ++x) {
+      if (j[x] < 0) continue;
+      const int to = (i0 + x * PASS) & (page - 1);
+      const int64_t dst = ((int64_t)dp[x] * a.c.page_stride + h * a.c.hs + to * a.c.rs) * esize + lane * 16;
+      const int64_t ds = ((int64_t)dp[x] * a.c.H + h) * page + to;
+      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.c.k) + dst) = kx[x];
+      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.c.v) + dst) = vx[x];
+      if (lane == 0) a.c.weight[ds] = f[x];
+      if (a.quantized && lane == 1) a.c.ks[ds] = f[x];
+      if (a.quantized && lane == 2) a.c.vs[ds] = f[x];
+    }
   }
+}
+
+template <int D, bool QUANT, bool FP16>
+cudaError_t launch_append_t(const AppendArgs& a, cudaStream_t st) {
+  constexpr int PASS = kAppendThreads / (D / 8);
+  const int64_t rows = (int64_t)a.T * a.c.H;
+  // four rows a thread once that leaves every SM a few CTAs
+  if (rows * a.c.B >= (int64_t)4 * PASS * 148 * 4) {
+    const dim3 grid((unsigned)((rows + 4 * PASS - 1) / (4 * PASS)), (unsigned)a.c.B);
+    kv_append_kernel<D, QUANT, FP16, 4><<<grid, kAppendThreads, 0, st>>>(a);
+  } else {
+    const dim3 grid((unsigned)((rows + PASS - 1) / PASS), (unsigned)a.c.B);
+    kv_append_kernel<D, QUANT, FP16, 1><<<grid, kAppendThreads, 0, st>>>(a);
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t st) {
-  const int L = a.c.D / 8;
-  const int64_t rows = (int64_t)a.c.B * a.T * a.c.H;
-  const dim3 grid((unsigned)((rows * L + kAppendThreads - 1) / kAppendThreads), 2);
-  if (rows == 0) return cudaSuccess;
+  if (a.T == 0) return cudaSuccess;
   if (a.c.D == 128) {
-    if (!a.quantized) kv_append_kernel<128, false, false><<<grid, kAppendThreads, 0, st>>>(a);
-    else if (a.is_fp16) kv_append_kernel<128, true, true><<<grid, kAppendThreads, 0, st>>>(a);
-    else kv_append_kernel<128, true, false><<<grid, kAppendThreads, 0, st>>>(a);
-  } else {
-    if (!a.quantized) kv_append_kernel<64, false, false><<<grid, kAppendThreads, 0, st>>>(a);
-    else if (a.is_fp16) kv_append_kernel<64, true, true><<<grid, kAppendThreads, 0, st>>>(a);
-    else kv_append_kernel<64, true, false><<<grid, kAppendThreads, 0, st>>>(a);
+    if (!a.quantized) return launch_append_t<128, false, false>(a, st);
+    return a.is_fp16 ? launch_append_t<128, true, true>(a, st) : launch_append_t<128, true, false>(a, st);
   }
-  return cudaGetLastError();
+  if (!a.quantized) return launch_append_t<64, false, false>(a, st);
+  return a.is_fp16 ? launch_append_t<64, true, true>(a, st) : launch_append_t<64, true, false>(a, st);
 }
 
-cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t st) {
+cudaError_t launch_kv_evict(const EvictArgs& args, cudaStream_t st) {
+  EvictArgs a = args;
   const int rows = a.c.B * a.c.H;
-  kv_select_kernel<<<rows, kSelThreads, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  static DeviceOnce once;
+  cudaError_t e = once.run([&](int) {
+    return cudaFuncSetAttribute(kv_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kSelKeys);
+  });
   if (e != cudaSuccess) return e;
+  // room for the keys of the longest sequence that the table can hold: less lets more CTAs share an SM
+  const int64_t most = (int64_t)a.c.cap - a.sinks - a.recent;
+  a.held_keys = (int)(most < 0 ? 0 : most > kSelKeys ? kSelKeys : most);
+  kv_select_kernel<<<rows, kSelThreads, (size_t)4 * a.held_keys, st>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int row_bytes = a.c.D * (a.quantized ? 1 : 2);
-  const int rpc = kMoveThreads / (row_bytes / 16);
-  const int want = (a.keep + rpc - 1) / rpc;
+  const int rpc = kMoveThreads / (row_bytes / 16) * kMoveRows;
+  const int64_t want = ((int64_t)a.keep + rpc - 1) / rpc;
   const dim3 grid((unsigned)rows, (unsigned)(want < 65535 ? want : 65535));
   switch (row_bytes) {
     case 256: return launch_pdl(kv_move_kernel<256>, grid, dim3(kMoveThreads), 0, st, a);

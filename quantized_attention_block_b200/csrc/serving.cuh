@@ -67,6 +67,7 @@ struct EvictArgs {
   int* new_lens;
   int* kept;
   int quantized;
+  int held_keys;  // set at launch: weights that the selection keeps in shared memory
 };
 
 struct WindowArgs {
