@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const EvictArgs 
 
 // Moves the rows that stay.  One row of K or V is ROW_BYTES / 16 lanes; a thread
 // has its 16 bytes of K and V of four rows in flight.
-constexpr int kMoveThreads = 256, kMoveRows = 4;
+constexpr int kMoveThreads = 128, kMoveRows = 2;
 
 template <int ROW_BYTES>
 __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictArgs a) {
@@ -307,8 +307,8 @@ __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictArgs a
       const int so = j[x] & (page - 1);
       const int64_t src = ((int64_t)sp[x] * a.c.page_stride + h * a.c.hs + so * a.c.rs) * esize + lane * 16;
       const int64_t ss = ((int64_t)sp[x] * a.c.H + h) * page + so;
-      kx[x] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.c.k) + src);
-      vx[x] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.c.v) + src);
+      kx[x] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.c.k) + src));
+      vx[x] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.c.v) + src));
       if (lane == 0) f[x] = a.c.weight[ss];
       if (a.quantized && lane == 1) f[x] = a.c.ks[ss];
       if (a.quantized && lane == 2) f[x] = a.c.vs[ss];
@@ -319,8 +319,8 @@ __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictArgs a
       const int to = (i0 + x * PASS) & (page - 1);
       const int64_t dst = ((int64_t)dp[x] * a.c.page_stride + h * a.c.hs + to * a.c.rs) * esize + lane * 16;
       const int64_t ds = ((int64_t)dp[x] * a.c.H + h) * page + to;
-      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.c.k) + dst) = kx[x];
-      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.c.v) + dst) = vx[x];
+      __stcs(reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.c.k) + dst), kx[x]);
+      __stcs(reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.c.v) + dst), vx[x]);
       if (lane == 0) a.c.weight[ds] = f[x];
       if (a.quantized && lane == 1) a.c.ks[ds] = f[x];
       if (a.quantized && lane == 2) a.c.vs[ds] = f[x];
