@@ -710,9 +710,12 @@ template <typename T, int D>
 cudaError_t launch_window_t(WindowArgs a, cudaStream_t st) {
   CUtensorMap q, k, v, kn, vn;
   if (!map_window(&q, a.q, D, a.N, a.Hq, a.B, a.nhd, 128) || !map_window(&k, a.k, D, a.N, a.Hkv, a.B, a.nhd, 128) ||
-      !map_window(&v, a.v, D, a.N, a.Hkv, a.B, a.nhd, 128) ||
-      !map_window(&kn, a.k, D, a.N, a.Hkv, a.B, a.nhd, kStep) ||
-      !map_window(&vn, a.v, D, a.N, a.Hkv, a.B, a.nhd, kStep))
+      !map_window(&v, a.v, D, a.N, a.Hkv, a.B, a.nhd, 128))
+    return cudaErrorInvalidValue;
+  kn = k, vn = v;
+  if (a.sinks > 0 && (a.sinks - 1) % 128 < kStep &&
+      (!map_window(&kn, a.k, D, a.N, a.Hkv, a.B, a.nhd, kStep) ||
+       !map_window(&vn, a.v, D, a.N, a.Hkv, a.B, a.nhd, kStep)))
     return cudaErrorInvalidValue;
   auto kernel = attn_window_kernel<T, D>;
   static DeviceOnce once;

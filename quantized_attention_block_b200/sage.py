@@ -459,41 +459,27 @@ def _layout(tensor_layout: str) -> int:
     return LAYOUTS[tensor_layout]
 
 
-def _range32(**ns) -> None:
-    for name, n in ns.items():
-        if not 0 <= n < 2 ** 31:
-            raise ValueError(f"{name} must be in [0, 2^31), got {n}")
-
-
-class _On:
-    """Work on a device (by number) and a stream (None: the device's current one): `raw` for the library; tensors
-    made inside belong to both.  Switches to them only if they are not current: the smallest calls take less time
-    than torch's own guards."""
-
-    __slots__ = ("raw", "guards")
-
-    def __init__(self, index: int, stream: Optional[torch.cuda.Stream]):
-        self.guards = []
-        if index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(index))
-        if stream is None:
-            self.raw = torch.cuda.current_stream(index).cuda_stream if _raw_stream is None else _raw_stream(index)
-        else:
-            self.guards.append(torch.cuda.stream(stream))
-            self.raw = stream.cuda_stream
-
-    def __enter__(self) -> int:
-        for g in self.guards:
-            g.__enter__()
-        return self.raw
-
-    def __exit__(self, *exc) -> None:
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+def _range32(names: str, *ns) -> None:
+    for n in ns:
+        if not 0 <= n < 2147483648:
+            raise ValueError(f"{names} must be in [0, 2^31), got {ns}")
 
 
 # torch's own handle of a device's current stream, without the Stream object around it
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on(index: int, stream: Optional[torch.cuda.Stream], work):
+    """work(raw stream) on a device (by number) and a stream (None: the device's current one), which are current
+    meanwhile, so that tensors made there belong to both."""
+    if stream is None:
+        if index == torch.cuda.current_device():
+            return work(_raw_stream(index))
+        with torch.cuda.device(index):
+            return work(_raw_stream(index))
+    with torch.cuda.device(index), torch.cuda.stream(stream):
+        return work(stream.cuda_stream)
 
 
 class KVCache:
@@ -530,7 +516,7 @@ class KVCache:
         self.k_pages, self.v_pages, self.k_scale, self.v_scale, self.weight = k_pages, v_pages, k_scale, v_scale, weight
         self.n_pages, self.Hkv, self.page_size, self.d, self.tensor_layout = n_pages, heads, page, d, tensor_layout
         self.device = k_pages.device
-        self._index = k_pages.get_device()
+        self._ws_bytes, self._no_workspace = {}, torch.empty(256, dtype=torch.uint8, device=self.device)
         for t in (v_pages, k_scale, v_scale, weight):
             if t is not None and t.device != self.device:
                 raise ValueError(f"the cache's tensors must be on one device, got {self.device} and {t.device}")
@@ -555,6 +541,16 @@ class KVCache:
         if dtype not in self._c:
             raise ValueError(f"the cache takes tokens of {' or '.join(map(str, self._c))}, got {dtype}")
         return self._c[dtype]
+
+    def _workspace(self, q, s: SageKvSeqs, p: SageDecodeParams, args) -> torch.Tensor:
+        """A workspace for a decode of these sizes (the number of bytes goes by them alone)."""
+        key = s.B, s.max_pages, p.Hq, p.window, p.sinks
+        n = self._ws_bytes.get(key)
+        if n is None:
+            n = self._ws_bytes[key] = int(lib().sage_decode_workspace_bytes(*args))
+        if n <= 256:  # nothing is kept there: any place will do
+            return self._no_workspace
+        return q.new_empty((n,), dtype=torch.uint8)
 
     def _seqs(self, page_table, lens) -> SageKvSeqs:
         if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
@@ -586,14 +582,14 @@ def sage_kv_append(k, v, cache: KVCache, page_table, lens, *, n_new=None, km=Non
             raise ValueError("km goes with a quantized cache")
         _expect("km", km, (s.B, cache.Hkv, cache.d), torch.float32)
     index = _one_device("cache, k, v, page_table, lens, n_new, km", cache.k_pages, k, v, page_table, lens, n_new, km)
-    with _On(index, stream) as raw:
-        _check(lib().sage_kv_append(k.data_ptr(), v.data_ptr(), _ptr(n_new), _ptr(km), T, layout, ctypes.byref(c),
-                                    ctypes.byref(s), raw), "sage_kv_append")
+    _on(index, stream, lambda raw: _check(
+        lib().sage_kv_append(k.data_ptr(), v.data_ptr(), _ptr(n_new), _ptr(km), T, layout, ctypes.byref(c),
+                             ctypes.byref(s), raw), "sage_kv_append"))
 
 
 def decode_workspace_bytes(cache: KVCache, page_table, lens, Hq: int, *, window: int = 0, sinks: int = 0) -> int:
     """Bytes of workspace of sage_attn_decode for these sizes (0: invalid)."""
-    _range32(window=window, sinks=sinks)
+    _range32("window, sinks", window, sinks)
     p = SageDecodeParams(Hq, window, sinks, 0.0)
     c = next(iter(cache._c.values()))
     return int(lib().sage_decode_workspace_bytes(ctypes.byref(c), ctypes.byref(cache._seqs(page_table, lens)),
@@ -601,7 +597,7 @@ def decode_workspace_bytes(cache: KVCache, page_table, lens, Hq: int, *, window:
 
 
 def _decode(q, cache, page_table, lens, window, sinks, sm_scale, km, out, lse, want_lse, workspace, stream):
-    _range32(window=window, sinks=sinks)
+    _range32("window, sinks", window, sinks)
     c, s = cache._struct(q.dtype), cache._seqs(page_table, lens)
     Hq = q.shape[1] if q.dim() == 3 else 0
     _expect("q", q, (s.B, Hq, cache.d), q.dtype)
@@ -620,18 +616,17 @@ def _decode(q, cache, page_table, lens, window, sinks, sm_scale, km, out, lse, w
     index = _one_device("cache, q, page_table, lens, km, out, lse, workspace", cache.k_pages, q, page_table, lens, km,
                         out, lse, workspace)
     p = SageDecodeParams(Hq, window, sinks, float(sm_scale if sm_scale else 0.0))
-    L = lib()
     args = ctypes.byref(c), ctypes.byref(s), ctypes.byref(p)
-    with _On(index, stream) as raw:
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None and want_lse:
-            lse = q.new_empty((s.B, Hq), dtype=torch.float32)
-        if workspace is None:
-            workspace = q.new_empty((L.sage_decode_workspace_bytes(*args),), dtype=torch.uint8)
-        _check(L.sage_attn_decode(q.data_ptr(), out.data_ptr(), _ptr(lse), _ptr(km), *args, workspace.data_ptr(),
-                                  workspace.numel(), raw), "sage_attn_decode")
-    return out, lse
+
+    def work(raw):
+        o = torch.empty_like(q) if out is None else out
+        z = q.new_empty((s.B, Hq), dtype=torch.float32) if lse is None and want_lse else lse
+        ws = cache._workspace(q, s, p, args) if workspace is None else workspace
+        _check(lib().sage_attn_decode(q.data_ptr(), o.data_ptr(), _ptr(z), _ptr(km), *args, ws.data_ptr(), ws.numel(),
+                                      raw), "sage_attn_decode")
+        return o, z
+
+    return _on(index, stream, work)
 
 
 def sage_attn_decode(q, cache: KVCache, page_table, lens, *, window: int = 0, sinks: int = 0,
@@ -659,7 +654,7 @@ def sage_kv_evict(cache: KVCache, page_table, lens, dst_table, keep: int, *, sin
     which no sequence may be using.  Returns (new_lens [B], kept [B,Hkv,keep]: old positions, -1 behind)."""
     if cache.weight is None:
         raise ValueError("the cache does not track weights")
-    _range32(keep=keep, sinks=sinks, recent=recent)
+    _range32("keep, sinks, recent", keep, sinks, recent)
     if keep < 1 or sinks + recent > keep:
         raise ValueError(f"keep must be at least 1 and hold sinks and recent, got {keep}, {sinks}, {recent}")
     c, s = next(iter(cache._c.values())), cache._seqs(page_table, lens)
@@ -673,19 +668,20 @@ def sage_kv_evict(cache: KVCache, page_table, lens, dst_table, keep: int, *, sin
         _expect("kept", kept, (s.B, cache.Hkv, keep), torch.int32)
     index = _one_device("cache, page_table, lens, dst_table, new_lens, kept", cache.k_pages, page_table, lens,
                         dst_table, new_lens, kept)
-    with _On(index, stream) as raw:
-        if new_lens is None:
-            new_lens = torch.empty_like(lens)
-        if kept is None:
-            kept = lens.new_empty((s.B, cache.Hkv, keep))
+
+    def work(raw):
+        n = torch.empty_like(lens) if new_lens is None else new_lens
+        at = lens.new_empty((s.B, cache.Hkv, keep)) if kept is None else kept
         _check(lib().sage_kv_evict(ctypes.byref(c), ctypes.byref(s), dst_table.data_ptr(), dst_table.shape[1], keep,
-                                   sinks, recent, new_lens.data_ptr(), kept.data_ptr(), raw), "sage_kv_evict")
-    return new_lens, kept
+                                   sinks, recent, n.data_ptr(), at.data_ptr(), raw), "sage_kv_evict")
+        return n, at
+
+    return _on(index, stream, work)
 
 
 def _window_fwd(q, k, v, window, sinks, lens, sm_scale, out, lse, want_lse, stream, tensor_layout):
     layout = _layout(tensor_layout)
-    _range32(window=window, sinks=sinks)
+    _range32("window, sinks", window, sinks)
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError(f"q and k must have 4 dimensions, got {tuple(q.shape)} and {tuple(k.shape)}")
     if q.dtype not in _DTYPES:
@@ -707,14 +703,15 @@ def _window_fwd(q, k, v, window, sinks, lens, sm_scale, out, lse, want_lse, stre
     zero = 0 if lens is None else (1 if out is None else 0) | (2 if lse is None else 0)
     p = SageWindowParams(B, Hq, Hkv, N, d, _DTYPES[q.dtype], layout, window, sinks, float(sm_scale if sm_scale else 0.0),
                          zero)
-    with _On(index, stream) as raw:
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None and want_lse:
-            lse = q.new_empty((B, Hq, N), dtype=torch.float32)
-        _check(lib().sage_attn_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse),
-                                          _ptr(lens), ctypes.byref(p), raw), "sage_attn_window_fwd")
-    return out, lse
+
+    def work(raw):
+        o = torch.empty_like(q) if out is None else out
+        z = q.new_empty((B, Hq, N), dtype=torch.float32) if lse is None and want_lse else lse
+        _check(lib().sage_attn_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(z), _ptr(lens),
+                                          ctypes.byref(p), raw), "sage_attn_window_fwd")
+        return o, z
+
+    return _on(index, stream, work)
 
 
 def sage_attn_window_fwd(q, k, v, *, window: int, sinks: int = 0, lens=None, sm_scale: Optional[float] = None,
