@@ -428,9 +428,14 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         const WinSteps st(a, w, i);
         const bool rows = st.end > 0;
         ks.tile = vs.tile = 0;
-        skip(ks, rows ? st.first >> 1 : w.nt);
-        skip(vs, rows ? st.first >> 1 : w.nt);
+        // none of the item's rows are here: K and V in turn (the ring holds no third K while the first V is taken)
+        for (int j = 1; !rows && j <= w.nt; ++j) {
+          skip(ks, j);
+          skip(vs, j);
+        }
         if (!rows) continue;
+        skip(ks, st.first >> 1);
+        skip(vs, st.first >> 1);
         ok = ok && mbar_wait_warp(&bar.q_full[i], n_items & 1);
         int c = st.first, d = st.first;  // the next S, the next P V
         auto qk = [&] {  // S = Q K^T of step c
