@@ -11,6 +11,17 @@ namespace {
 
 using namespace sage;
 
+// check_arch() of the current device, asked once
+sage_status check_device() {
+  static DeviceOnce once;
+  int st = SAGE_OK;
+  const cudaError_t e = once.run([&](int dev) {
+    once.value[dev] = check_arch();
+    return once.value[dev] == SAGE_ERR_CUDA ? cudaErrorUnknown : cudaSuccess;
+  }, &st);
+  return e != cudaSuccess ? SAGE_ERR_CUDA : (sage_status)st;
+}
+
 sage_status check_cache(const sage_kv_cache* c, const sage_kv_seqs* s) {
   if (!c || !s) return SAGE_ERR_INVALID_ARG;
   if (c->Hkv < 1 || c->Hkv > 65535 || c->n_pages < 1 || s->B < 1 || s->B > 65535 || s->max_pages < 1)
@@ -115,7 +126,7 @@ sage_status sage_kv_append(const void* k, const void* v, const int32_t* n_new, c
   if ((st = check_cache_ptrs(c, s)) != SAGE_OK) return st;
   if (!aligned16(k) || !aligned16(v) || !aligned16(km) || (reinterpret_cast<uintptr_t>(n_new) & 3u))
     return SAGE_ERR_MISALIGNED;
-  if ((st = check_arch()) != SAGE_OK) return st;
+  if ((st = check_device()) != SAGE_OK) return st;
   AppendArgs a{};
   a.c = cache_args(c, s);
   a.k = k;
@@ -146,7 +157,7 @@ sage_status sage_attn_decode(const void* q, void* o, float* lse, const float* km
     return SAGE_ERR_MISALIGNED;
   const DecodeLayout L = decode_layout(c, s, p);
   if (workspace_bytes < L.total) return SAGE_ERR_WORKSPACE_TOO_SMALL;
-  if ((st = check_arch()) != SAGE_OK) return st;
+  if ((st = check_device()) != SAGE_OK) return st;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   DecodeArgs a{};
   a.c = cache_args(c, s);
@@ -188,7 +199,7 @@ sage_status sage_kv_evict(const sage_kv_cache* c, const sage_kv_seqs* s, const i
   if ((reinterpret_cast<uintptr_t>(dst_table) & 3u) || (reinterpret_cast<uintptr_t>(new_lens) & 3u) ||
       (reinterpret_cast<uintptr_t>(kept) & 3u))
     return SAGE_ERR_MISALIGNED;
-  if ((st = check_arch()) != SAGE_OK) return st;
+  if ((st = check_device()) != SAGE_OK) return st;
   EvictArgs a{};
   a.c = cache_args(c, s);
   a.dst_table = dst_table;
@@ -216,7 +227,7 @@ sage_status sage_attn_window_fwd(const void* q, const void* k, const void* v, vo
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
       (reinterpret_cast<uintptr_t>(lens) & 3u))
     return SAGE_ERR_MISALIGNED;
-  sage_status st = check_arch();
+  sage_status st = check_device();
   if (st != SAGE_OK) return st;
   WindowArgs a{};
   a.q = q;

@@ -430,7 +430,7 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 def _expect(name: str, t: torch.Tensor, shape, dtype) -> None:
     """A contiguous tensor of this shape (None: any extent) and type, else ValueError."""
-    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and t.is_contiguous():
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous():
         return
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
@@ -442,14 +442,14 @@ def _expect(name: str, t: torch.Tensor, shape, dtype) -> None:
         raise ValueError(f"{name} must be contiguous")
 
 
-def _one_device(names: str, *ts) -> int:
-    """The number of the CUDA device that all the tensors (None: absent) are on."""
-    index = ts[0].get_device()
+def _one_device(names: str, index: int, *ts) -> int:
+    """`index`, the number of the CUDA device that all the tensors (None: absent) must be on."""
     for t in ts:
         if t is not None and t.get_device() != index:
-            raise ValueError(f"{names} must be on one device, got {[str(x.device) for x in ts if x is not None]}")
-    if index < 0 or ts[0].device.type != "cuda":
-        raise ValueError(f"{names} must be on a CUDA device, got {ts[0].device}")
+            raise ValueError(f"{names} must be on one device, got {[str(x.device) for x in ts if x is not None]} "
+                             f"beside device {index}")
+    if index < 0:
+        raise ValueError(f"{names} must be on a CUDA device")
     return index
 
 
@@ -465,7 +465,9 @@ def _range32(names: str, *ns) -> None:
             raise ValueError(f"{names} must be in [0, 2^31), got {ns}")
 
 
-# torch's own handle of a device's current stream, without the Stream object around it
+# torch's own number of the current device and handle of a device's current stream, without the objects around
+# them (the tensors of the call are on a CUDA device, so CUDA is initialised)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -474,7 +476,7 @@ def _on(index: int, stream: Optional[torch.cuda.Stream], work):
     """work(raw stream) on a device (by number) and a stream (None: the device's current one), which are current
     meanwhile, so that tensors made there belong to both."""
     if stream is None:
-        if index == torch.cuda.current_device():
+        if index == _current_device():
             return work(_raw_stream(index))
         with torch.cuda.device(index):
             return work(_raw_stream(index))
@@ -516,6 +518,7 @@ class KVCache:
         self.k_pages, self.v_pages, self.k_scale, self.v_scale, self.weight = k_pages, v_pages, k_scale, v_scale, weight
         self.n_pages, self.Hkv, self.page_size, self.d, self.tensor_layout = n_pages, heads, page, d, tensor_layout
         self.device = k_pages.device
+        self._index = k_pages.get_device() if k_pages.is_cuda else -1
         self._ws_bytes, self._no_workspace = {}, torch.empty(256, dtype=torch.uint8, device=self.device)
         for t in (v_pages, k_scale, v_scale, weight):
             if t is not None and t.device != self.device:
@@ -553,13 +556,13 @@ class KVCache:
         return q.new_empty((n,), dtype=torch.uint8)
 
     def _seqs(self, page_table, lens) -> SageKvSeqs:
-        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        shape = page_table.shape if isinstance(page_table, torch.Tensor) else ()
+        if len(shape) != 2 or page_table.dtype is not torch.int32 or not page_table.is_contiguous():
             _expect("page_table", page_table, (None, None), torch.int32)
-        B, max_pages = page_table.shape
-        _expect("page_table", page_table, (B, max_pages), torch.int32)
+        B, max_pages = shape
         _expect("lens", lens, (B,), torch.int32)
         if B < 1 or max_pages < 1:
-            raise ValueError(f"page_table must not be empty, got {tuple(page_table.shape)}")
+            raise ValueError(f"page_table must not be empty, got {tuple(shape)}")
         return SageKvSeqs(B, max_pages, page_table.data_ptr(), lens.data_ptr())
 
 
@@ -581,7 +584,7 @@ def sage_kv_append(k, v, cache: KVCache, page_table, lens, *, n_new=None, km=Non
         if not cache.quantized:
             raise ValueError("km goes with a quantized cache")
         _expect("km", km, (s.B, cache.Hkv, cache.d), torch.float32)
-    index = _one_device("cache, k, v, page_table, lens, n_new, km", cache.k_pages, k, v, page_table, lens, n_new, km)
+    index = _one_device("cache, k, v, page_table, lens, n_new, km", cache._index, k, v, page_table, lens, n_new, km)
     _on(index, stream, lambda raw: _check(
         lib().sage_kv_append(k.data_ptr(), v.data_ptr(), _ptr(n_new), _ptr(km), T, layout, ctypes.byref(c),
                              ctypes.byref(s), raw), "sage_kv_append"))
@@ -613,7 +616,7 @@ def _decode(q, cache, page_table, lens, window, sinks, sm_scale, km, out, lse, w
         _expect("km", km, (s.B, cache.Hkv, cache.d), torch.float32)
     if workspace is not None:
         _expect("workspace", workspace, (workspace.numel(),), torch.uint8)
-    index = _one_device("cache, q, page_table, lens, km, out, lse, workspace", cache.k_pages, q, page_table, lens, km,
+    index = _one_device("cache, q, page_table, lens, km, out, lse, workspace", cache._index, q, page_table, lens, km,
                         out, lse, workspace)
     p = SageDecodeParams(Hq, window, sinks, float(sm_scale if sm_scale else 0.0))
     args = ctypes.byref(c), ctypes.byref(s), ctypes.byref(p)
@@ -666,7 +669,7 @@ def sage_kv_evict(cache: KVCache, page_table, lens, dst_table, keep: int, *, sin
         _expect("new_lens", new_lens, (s.B,), torch.int32)
     if kept is not None:
         _expect("kept", kept, (s.B, cache.Hkv, keep), torch.int32)
-    index = _one_device("cache, page_table, lens, dst_table, new_lens, kept", cache.k_pages, page_table, lens,
+    index = _one_device("cache, page_table, lens, dst_table, new_lens, kept", cache._index, page_table, lens,
                         dst_table, new_lens, kept)
 
     def work(raw):
@@ -698,7 +701,7 @@ def _window_fwd(q, k, v, window, sinks, lens, sm_scale, out, lse, want_lse, stre
         _expect("out", out, q.shape, q.dtype)
     if lse is not None:
         _expect("lse", lse, (B, Hq, N), torch.float32)
-    index = _one_device("q, k, v, lens, out, lse", q, k, v, lens, out, lse)
+    index = _one_device("q, k, v, lens, out, lse", q.get_device(), k, v, lens, out, lse)
     # rows behind a sequence's end are not written: zeros in tensors made here
     zero = 0 if lens is None else (1 if out is None else 0) | (2 if lse is None else 0)
     p = SageWindowParams(B, Hq, Hkv, N, d, _DTYPES[q.dtype], layout, window, sinks, float(sm_scale if sm_scale else 0.0),
