@@ -702,11 +702,15 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
 }
 
 // Joins the pieces of a row in the order of their CTAs; one CTA a (sequence,
-// query head).  Rows that one CTA did alone are done already.
-template <int D, int MT>
-__global__ void __launch_bounds__(128) decode_join_kernel(const DecodeArgs a) {
+// query head).  Rows that one CTA did alone are done already.  A few long rows
+// have a piece for every CTA of the split, which 512 threads read four (D = 128)
+// at a time: 64 us against 72 with 128 threads for 32 heads over 131k tokens.
+// Many rows have a piece or two each: 284 us with 128 threads against 299 for
+// 64 x 64 heads.
+template <int D, int MT, int kJoinThreads>
+__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeArgs a) {
   __shared__ float s_f[kDecodeCtas];
-  __shared__ float s_x[128];
+  __shared__ float s_x[kJoinThreads], s_w[kJoinThreads / 32];
   pdl_launch();
   pdl_wait();
   const int tid = threadIdx.x;
@@ -715,7 +719,7 @@ __global__ void __launch_bounds__(128) decode_join_kernel(const DecodeArgs a) {
   const int vb = visible_span(cache_len(a.c, b), a.window, a.sinks).vb;
   const int64_t out = ((int64_t)b * a.Hq + hq) * D;
   if (vb == 0) {
-    for (int d = tid; d < D; d += 128) store16(a.o, out + d, 0.0f, a.q_fp16);
+    if (tid < D) store16(a.o, out + tid, 0.0f, a.q_fp16);
     if (tid < 32) write_lse<D>(a, b, hq, -INFINITY, 0.0f);
     return;
   }
@@ -724,43 +728,42 @@ __global__ void __launch_bounds__(128) decode_join_kernel(const DecodeArgs a) {
   const int c0 = (int)(u / share), c1 = (int)((u + vb - 1) / share), n = c1 - c0 + 1;
   if (n == 1) return;
   auto slot = [&](int i) { return 2 * (c0 + i) + (i == 0 && u != c0 * share ? 1 : 0); };
+  // of x over the CTA: sum or maximum
+  auto all = [&](float x, auto f) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x = f(x, __shfl_xor_sync(0xffffffffu, x, d));
+    __syncthreads();
+    if ((tid & 31) == 0) s_w[tid >> 5] = x;
+    __syncthreads();
+    x = s_w[0];
+#pragma unroll
+    for (int w = 1; w < kJoinThreads / 32; ++w) x = f(x, s_w[w]);
+    return x;
+  };
   // largest m, factors of the pieces, l
   float mx = -INFINITY;
-  for (int i = tid; i < n; i += 128) mx = fmaxf(mx, a.part_m[slot(i) * kMaxGroup + r]);
-  s_x[tid] = mx;
-  __syncthreads();
-  for (int i = 64; i > 0; i >>= 1) {
-    if (tid < i) s_x[tid] = fmaxf(s_x[tid], s_x[tid + i]);
-    __syncthreads();
-  }
-  mx = s_x[0];
-  __syncthreads();
+  for (int i = tid; i < n; i += kJoinThreads) mx = fmaxf(mx, a.part_m[slot(i) * kMaxGroup + r]);
+  mx = all(mx, [](float x, float y) { return fmaxf(x, y); });
   const float ms = mx == -INFINITY ? 0.0f : mx;
   float l = 0.0f;
-  for (int i = tid; i < n; i += 128) {
+  for (int i = tid; i < n; i += kJoinThreads) {
     const float f = exp2f(a.part_m[slot(i) * kMaxGroup + r] - ms);
     s_f[i] = f;
     l += f * a.part_l[slot(i) * kMaxGroup + r];
   }
-  s_x[tid] = l;
-  __syncthreads();
-  for (int i = 64; i > 0; i >>= 1) {
-    if (tid < i) s_x[tid] += s_x[tid + i];
-    __syncthreads();
-  }
-  l = s_x[0];
-  __syncthreads();
-  constexpr int P = 128 / D;  // pieces summed side by side
+  l = all(l, [](float x, float y) { return x + y; });
+  constexpr int P = kJoinThreads / D;  // pieces summed side by side
   const int d = tid % D;
   float x = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = tid / D; i < n; i += P) x += s_f[i] * a.part_o[((int64_t)slot(i) * kMaxGroup + r) * D + d];
-  if constexpr (P > 1) {
-    s_x[tid] = x;
-    __syncthreads();
-    if (tid < D) x += s_x[tid + D];
+  s_x[tid] = x;
+  __syncthreads();
+  if (tid < D) {
+#pragma unroll
+    for (int p = 1; p < P; ++p) x += s_x[tid + p * D];
+    store16(a.o, out + d, l > 0.0f || isnan(l) ? x / l : 0.0f, a.q_fp16);
   }
-  if (tid < D) store16(a.o, out + d, l > 0.0f || isnan(l) ? x / l : 0.0f, a.q_fp16);
   if (tid < 32) write_lse<D>(a, b, hq, mx, l);
 }
 
@@ -810,7 +813,9 @@ cudaError_t launch_decode_t(const DecodeArgs& a, cudaStream_t st) {
   if (ctas > kDecodeCtas) ctas = kDecodeCtas;
   kernel<<<(unsigned)ctas, kDecThreads, smem, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  e = launch_pdl(decode_join_kernel<D, MT>, dim3((unsigned)(a.c.B * a.Hq)), dim3(128), 0, st, a);
+  const int64_t heads = (int64_t)a.c.B * a.Hq;
+  e = heads <= 296 ? launch_pdl(decode_join_kernel<D, MT, 512>, dim3((unsigned)heads), dim3(512), 0, st, a)
+                   : launch_pdl(decode_join_kernel<D, MT, 128>, dim3((unsigned)heads), dim3(128), 0, st, a);
   if (e != cudaSuccess || !a.scores) return e;
   return launch_pdl(decode_weight_kernel, weights, dim3(256), 0, st, a);
 }
