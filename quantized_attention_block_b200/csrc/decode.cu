@@ -169,18 +169,44 @@ __device__ __forceinline__ void write_lse(const DecodeArgs& a, int b, int hq, fl
   }
 }
 
-// weight of the i-th visible slot of (b, h) += sum over the group's heads of 2^(t - lse2)
+// weight of the visible slots first, first + stride, ... of (b, h) += sum over the group's heads of 2^(t - lse2);
+// four at a time, so that their page numbers and weights are on the way together (9 of 26 us one by one, for
+// 384 heads that see 1028 keys)
 template <typename F>
-__device__ __forceinline__ void add_weight(const DecodeArgs& a, const Span& sp, int b, int h, int i, F lse2) {
-  const int page = 1 << a.c.page_log2;
-  const int j = span_block(sp, i / kBlk) * kBlk + i % kBlk;
-  if (j >= sp.n || (j < sp.ws && j >= a.sinks)) return;
-  const int pid = a.c.table[(int64_t)b * a.c.max_pages + (j >> a.c.page_log2)];
-  if (pid < 0 || pid >= a.c.n_pages) return;
-  const float* t = a.scores + ((int64_t)b * a.Hq + h * a.G) * a.score_cap + i;
-  float x = 0.0f;
-  for (int g = 0; g < a.G; ++g) x += exp2f(t[g * a.score_cap] - lse2(g));
-  a.c.weight[((int64_t)pid * a.c.H + h) * page + (j & (page - 1))] += x;
+__device__ __forceinline__ void add_weights(const DecodeArgs& a, const Span& sp, int b, int h, int first, int stride,
+                                            F lse2) {
+  constexpr int U = 4;
+  const int page = 1 << a.c.page_log2, end = sp.vb * kBlk;
+  const float* scores = a.scores + ((int64_t)b * a.Hq + h * a.G) * a.score_cap;
+  for (int i0 = first; i0 < end; i0 += U * stride) {
+    int j[U], pid[U];
+    float* w[U];
+    float x[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int i = i0 + k * stride;
+      j[k] = i < end ? span_block(sp, i / kBlk) * kBlk + i % kBlk : sp.n;
+      if (j[k] >= sp.n || (j[k] < sp.ws && j[k] >= a.sinks)) pid[k] = -1;
+      else pid[k] = __ldg(a.c.table + (int64_t)b * a.c.max_pages + (j[k] >> a.c.page_log2));
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      w[k] = nullptr;
+      x[k] = 0.0f;
+      if ((uint32_t)pid[k] < (uint32_t)a.c.n_pages) {
+        w[k] = a.c.weight + ((int64_t)pid[k] * a.c.H + h) * page + (j[k] & (page - 1));
+        x[k] = *w[k];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (!w[k]) continue;
+      const float* t = scores + i0 + k * stride;
+      float y = 0.0f;
+      for (int g = 0; g < a.G; ++g) y += exp2f(t[g * a.score_cap] - lse2(g));
+      *w[k] = x[k] + y;
+    }
+  }
 }
 
 // register i of Q's fragment; with 8 heads a row, rows 8-15 are zeros
@@ -688,8 +714,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
     }
     __syncthreads();  // the rings may be filled again
     if (!SPLIT && a.scores && a.GT == 1) {  // (more tiles of a group share the weights: decode_weight_kernel)
-      for (int i = tid; i < sp.vb * kBlk; i += kDecThreads)
-        add_weight(a, sp, b, h, i, [&](int g) { return s_lse[g]; });
+      add_weights(a, sp, b, h, tid, kDecThreads, [&](int g) { return s_lse[g]; });
     }
     u += nblk;
     off += nblk;
@@ -767,21 +792,20 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeA
   if (tid < 32) write_lse<D>(a, b, hq, mx, l);
 }
 
-// the weights of all keys, one thread a key
+// the weights of all keys
 __global__ void __launch_bounds__(256) decode_weight_kernel(const DecodeArgs a) {
   pdl_wait();
   const int b = blockIdx.x / a.c.H, h = blockIdx.x % a.c.H;
   const Span sp = visible_span(cache_len(a.c, b), a.window, a.sinks);
   const float* lse2 = a.lse2 + (int64_t)b * a.Hq + h * a.G;
-  for (int i = blockIdx.y * 256 + threadIdx.x; i < sp.vb * kBlk; i += gridDim.y * 256)
-    add_weight(a, sp, b, h, i, [&](int g) { return lse2[g]; });
+  add_weights(a, sp, b, h, blockIdx.y * 256 + threadIdx.x, gridDim.y * 256, [&](int g) { return lse2[g]; });
 }
 
 template <int D, int CT, int MT>
 cudaError_t launch_decode_t(const DecodeArgs& a, cudaStream_t st) {
   constexpr int smem = kDecWarps * DecTile<D, CT>::kWarpBytes;
   static_assert(MT * D * 4 <= DecTile<D, CT>::kWarpBytes, "a warp's ring holds its rows of O for the merge");
-  const int64_t want = (a.score_cap + 255) / 256;
+  const int64_t want = (a.score_cap + 1023) / 1024;  // four keys a thread
   const dim3 weights((unsigned)(a.c.B * a.c.H), (unsigned)(want < 64 ? want : 64));
   cudaError_t e;
   if (a.direct) {
