@@ -37,7 +37,7 @@ namespace {
 
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
-constexpr int kMinShare = 4;  // blocks of the smallest share: one a warp
+constexpr int kMinShare = 8;  // blocks of the smallest share: two a warp (4k tokens of 8 heads: 14.0 us with 4, 12.7 with 8, 13.8 with 16)
 
 enum CacheType : int { kBF16 = 0, kFP16 = 1, kQ8 = 2 };
 
