@@ -474,8 +474,8 @@ SAGE_API size_t sage_decode_workspace_bytes(const sage_kv_cache *c, const sage_k
  * lens[b] == 0: o = 0 and lse = -infinity.  km (device fp32 [B, Hkv, d] or
  * NULL; quantized caches): lse += sm_scale q . km, for the keys as they were
  * before km was taken off.  With c->weight, every visible key's weight grows by
- * sum over the query heads of its group of exp(S_j - lse); sequences of one call
- * must not share pages then.
+ * sum over the query heads of its group of exp(S_j - lse); sequences of one call,
+ * and of calls that run at the same time, must not share pages then.
  * Softmax statistics and sums are held in fp32; the weights of V enter the
  * tensor cores as two 16-bit numbers that together carry 16 bits or more.
  * Results do not depend on scheduling (no atomics): the same inputs give the

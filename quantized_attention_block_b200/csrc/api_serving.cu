@@ -17,7 +17,7 @@ sage_status check_device() {
   int st = SAGE_OK;
   const cudaError_t e = once.run([&](int dev) {
     once.value[dev] = check_arch();
-    return once.value[dev] == SAGE_ERR_CUDA ? cudaErrorUnknown : cudaSuccess;
+    return once.value[dev].load() == SAGE_ERR_CUDA ? cudaErrorUnknown : cudaSuccess;
   }, &st);
   return e != cudaSuccess ? SAGE_ERR_CUDA : (sage_status)st;
 }
@@ -195,6 +195,7 @@ sage_status sage_kv_evict(const sage_kv_cache* c, const sage_kv_seqs* s, const i
   if (keep < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > keep) return SAGE_ERR_INVALID_ARG;
   if (dst_pages < 1 || (int64_t)dst_pages * c->page_size < keep) return SAGE_ERR_INVALID_ARG;
   if (dst_table == s->table || new_lens == s->lens) return SAGE_ERR_INVALID_ARG;
+  if ((int64_t)s->B * c->Hkv >= (int64_t(1) << 31)) return SAGE_ERR_INVALID_ARG;
   if ((st = check_cache_ptrs(c, s)) != SAGE_OK) return st;
   if ((reinterpret_cast<uintptr_t>(dst_table) & 3u) || (reinterpret_cast<uintptr_t>(new_lens) & 3u) ||
       (reinterpret_cast<uintptr_t>(kept) & 3u))

@@ -21,11 +21,11 @@
 // A step of a row tile is 64 keys: S = Q K^T, softmax, O += P V.  TMEM (512
 // columns): two buffers of S a row tile, at 128 i + 64 b, with P (16 bit, the A
 // operand of P V) over the first half of its S; O_i at 256 + D i.  S of the next
-// step is computed while the softmax works on this one, so a row's chain never
-// waits for the tensor core.  (Steps of 128 keys, whose S fills the columns that
-// both buffers have here, left the softmax waiting 1400 of 4000 cycles for
-// P V and the next S; N = 64 costs the Q K^T half of its rate instead, since A
-// and B then take 6 KB of shared memory for 32 cycles of products.)
+// step is computed while the softmax works on this one.  (Steps of 128 keys, whose
+// S fills the columns that both buffers have here, left the softmax waiting 1400 of
+// 4000 cycles for P V and the next S; now it waits 300 of 1880.  N = 64 costs the
+// Q K^T a third of its rate: A and B then take 6 KB of shared memory for 32 cycles
+// of products.)
 // Each row tile has an issuing warp of its own: one thread that polled for both
 // spent longer on its bookkeeping (some 2500 cycles for 128 keys) than the tensor
 // core on the products.  The exponentials are the MUFU's alone: a polynomial on

@@ -96,7 +96,7 @@ cudaError_t launch_attn_window(const WindowArgs& a, int is_fp16, cudaStream_t st
 struct DeviceOnce {
   static constexpr int kDevices = 64;
   std::atomic<bool> done[kDevices] = {};
-  int value[kDevices] = {};  // what f(device) leaves there
+  std::atomic<int> value[kDevices] = {};  // what f(device) leaves there
   template <typename F>
   cudaError_t run(F&& f, int* got = nullptr) {
     int dev = 0;

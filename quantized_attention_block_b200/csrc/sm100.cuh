@@ -472,8 +472,8 @@ constexpr float kExp2C0 = 0.9999977946281433f, kExp2C1 = 0.693130612373352f, kEx
 __device__ __forceinline__ float2 exp2_poly2(float2 x) {
   x = make_float2(fmaxf(x.x, -126.0f), fmaxf(x.y, -126.0f));
   const float2 j = __fadd2_rn(x, make_float2(12582912.0f, 12582912.0f));
-  const float2 minus_n = __ffma2_rn(j, make_float2(-1.0f, -1.0f), make_float2(12582912.0f, 12582912.0f));
-  const float2 f = __fadd2_rn(x, minus_n);
+  const float2 n = __fadd2_rn(j, make_float2(-12582912.0f, -12582912.0f));
+  const float2 f = __fadd2_rn(x, make_float2(-n.x, -n.y));
   float2 p = __ffma2_rn(f, make_float2(kExp2C4, kExp2C4), make_float2(kExp2C3, kExp2C3));
   p = __ffma2_rn(f, p, make_float2(kExp2C2, kExp2C2));
   p = __ffma2_rn(f, p, make_float2(kExp2C1, kExp2C1));

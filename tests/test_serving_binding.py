@@ -23,6 +23,13 @@ def test_window_zero_tail_is_two_bits(L, zero_tail):
     assert L.sage_attn_window_fwd(P16, P16, P16, P16, None, P16, ctypes.byref(p), None) == 1
 
 
+def test_evict_counts_its_rows(L):
+    """Sequences times heads is the kernels' grid: below 2^31."""
+    c = sage.SageKvCache(65535, 64, 0, 0, 16, 8, 0, P16, P16, None, None, P16)
+    s = sage.SageKvSeqs(65535, 4, P16, P16)
+    assert L.sage_kv_evict(ctypes.byref(c), ctypes.byref(s), P16 + 64, 2, 32, 4, 8, P16 + 64, P16, None) == 1
+
+
 def workspace(L, max_pages, window=0, sinks=0, B=2, Hq=4, weight=None, page=16):
     c = sage.SageKvCache(2, 64, 0, 0, page, 8, 0, P16, P16, None, None, weight)
     s = sage.SageKvSeqs(B, max_pages, P16, P16)
