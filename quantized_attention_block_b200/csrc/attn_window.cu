@@ -559,12 +559,15 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       if (st.end == 0) continue;
       const int p0 = w.q0 + 128 * ti, p = p0 + row;
       float m = -INFINITY, l = 0.0f;
+      // steps from `diagonal` on hold keys behind the tile's first row; before `whole`, keys that its last row's
+      // window leaves out, unless the step is one of the first `whole_sinks`
+      const int diagonal = 2 * (w.ns + p0 / 128 - w.t0), whole_sinks = a.sinks / kStep;
+      const int out = p0 + 128 - a.window - 128 * (w.t0 - w.ns);
+      const int whole = a.window > 0 && p0 + 128 > a.window ? (out + kStep - 1) / kStep : 0;
       for (int u = st.first; u != st.end; u = st.next(u), ++step) {
         const uint32_t tS = tmem + 128 * ti + 64 * (step & 1) + lanes;
-        const int key0 = win_key(w, u);
-        // keys behind the first row's position, before the last row's window, or behind the sinks
-        const bool masked = key0 + kStep - 1 > p0 ||
-                            (a.window > 0 && p0 + 128 - a.window > key0 && a.sinks - key0 < kStep);
+        // keys behind the first row's position, or before the last row's window and not all sinks
+        const bool masked = u >= diagonal || (u >= whole_sinks && u < whole);
         if (!(ok = mbar_wait_warp(&bar.s_full[2 * ti + (step & 1)], (step >> 1) & 1))) break;
         tc_fence_after();
         uint32_t s[kStep];
@@ -573,7 +576,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         tmem_ld_wait();
         if (masked) {
           // columns c <= hi and (c >= lo or c < sk) are visible
-          const int hi = p - key0, lo = a.window > 0 ? hi - a.window + 1 : INT_MIN, sk = a.sinks - key0;
+          const int key0 = win_key(w, u), hi = p - key0, lo = a.window > 0 ? hi - a.window + 1 : INT_MIN, sk = a.sinks - key0;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const uint32_t see = low_bits(hi + 1 - 32 * x) & (~low_bits(lo - 32 * x) | low_bits(sk - 32 * x));

@@ -72,6 +72,12 @@ def test_steps_cover_the_visible_keys_once():
                     j = np.arange(k0, k0 + STEP)
                     visible = (j <= p[:, None]) & ((window == 0) | (p[:, None] - j < window) | (j < sinks))
                     masked = k0 + STEP - 1 > p0 or (w.window > 0 and p0 + 128 - w.window > k0 and w.sinks - k0 < STEP)
+                    # as the kernel has it, by the step's number
+                    diagonal = 2 * (w.ns + p0 // 128 - w.t0)
+                    whole = 0
+                    if w.window > 0 and p0 + 128 > w.window:
+                        whole = int((p0 + 128 - w.window - 128 * (w.t0 - w.ns) + STEP - 1) / STEP)
+                    assert masked == (u >= diagonal or w.sinks // STEP <= u < whole)
                     assert masked or visible.all(), (N, n, window, sinks, pair, i, u)
                     # a narrow tile holds its first 64 keys alone
                     assert u >> 1 != w.narrow or u & 1 == 0
