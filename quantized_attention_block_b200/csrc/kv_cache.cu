@@ -270,7 +270,9 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const EvictArgs 
 }
 
 // Moves the rows that stay.  One row of K or V is ROW_BYTES / 16 lanes; a thread
-// has its 16 bytes of K and V of four rows in flight.
+// has its 16 bytes of K and V of two rows in flight.  More are slower, not faster
+// (192 us in all with two, 246 with four, 321 with eight for 128 rows of up to
+// 12288 tokens), and so are accesses that stay in L2 (212 us).
 constexpr int kMoveThreads = 128, kMoveRows = 2;
 
 template <int ROW_BYTES>
@@ -283,10 +285,28 @@ __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictArgs a
   const int lane = threadIdx.x % L;
   const int page = 1 << a.c.page_log2;
   const int esize = a.quantized ? 1 : 2;
-  for (int i0 = blockIdx.y * (PASS * kMoveRows) + threadIdx.x / L; i0 < n; i0 += gridDim.y * (PASS * kMoveRows)) {
+  // weights and scales, a thread a row (a lane of each row's in the loop below: 198 us against 190 for 128 rows of up
+  // to 12288 tokens; bad pages are recorded there)
+  constexpr int ROWS = PASS * kMoveRows;  // of the CTA at a time
+  static_assert(ROWS <= kMoveThreads, "a thread a row");
+  for (int i = blockIdx.y * ROWS + threadIdx.x; threadIdx.x < ROWS && i < n; i += gridDim.y * ROWS) {
+    const int j = __ldg(a.kept + (int64_t)bh * a.keep + i);
+    const int sp = __ldg(a.c.table + (int64_t)b * a.c.max_pages + (j >> a.c.page_log2));
+    const int dp = __ldg(a.dst_table + (int64_t)b * a.dst_pages + (i >> a.c.page_log2));
+    if ((uint32_t)sp >= (uint32_t)a.c.n_pages || (uint32_t)dp >= (uint32_t)a.c.n_pages) continue;
+    const int64_t ss = ((int64_t)sp * a.c.H + h) * page + (j & (page - 1));
+    const int64_t ds = ((int64_t)dp * a.c.H + h) * page + (i & (page - 1));
+    const float w = a.c.weight[ss];
+    if (a.quantized) {
+      const float x = a.c.ks[ss], y = a.c.vs[ss];
+      a.c.ks[ds] = x;
+      a.c.vs[ds] = y;
+    }
+    a.c.weight[ds] = w;
+  }
+  for (int i0 = blockIdx.y * ROWS + threadIdx.x / L; i0 < n; i0 += gridDim.y * ROWS) {
     int j[kMoveRows], sp[kMoveRows], dp[kMoveRows];
     uint4 kx[kMoveRows], vx[kMoveRows];
-    float f[kMoveRows];  // lane 0: weight, 1 and 2: scales
 #pragma unroll
     for (int x = 0; x < kMoveRows; ++x) {
       const int i = i0 + x * PASS;
@@ -306,24 +326,16 @@ __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictArgs a
       }
       const int so = j[x] & (page - 1);
       const int64_t src = ((int64_t)sp[x] * a.c.page_stride + h * a.c.hs + so * a.c.rs) * esize + lane * 16;
-      const int64_t ss = ((int64_t)sp[x] * a.c.H + h) * page + so;
       kx[x] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.c.k) + src));
       vx[x] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.c.v) + src));
-      if (lane == 0) f[x] = a.c.weight[ss];
-      if (a.quantized && lane == 1) f[x] = a.c.ks[ss];
-      if (a.quantized && lane == 2) f[x] = a.c.vs[ss];
     }
 #pragma unroll
     for (int x = 0; x < kMoveRows; ++x) {
       if (j[x] < 0) continue;
       const int to = (i0 + x * PASS) & (page - 1);
       const int64_t dst = ((int64_t)dp[x] * a.c.page_stride + h * a.c.hs + to * a.c.rs) * esize + lane * 16;
-      const int64_t ds = ((int64_t)dp[x] * a.c.H + h) * page + to;
       __stcs(reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.c.k) + dst), kx[x]);
       __stcs(reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.c.v) + dst), vx[x]);
-      if (lane == 0) a.c.weight[ds] = f[x];
-      if (a.quantized && lane == 1) a.c.ks[ds] = f[x];
-      if (a.quantized && lane == 2) a.c.vs[ds] = f[x];
     }
   }
 }
