@@ -541,16 +541,16 @@ class KVCache:
         return cls(k, v, *s, w, tensor_layout=tensor_layout)
 
     def _struct(self, dtype) -> SageKvCache:
-        if dtype not in self._c:
+        c = self._c.get(dtype)
+        if c is None:
             raise ValueError(f"the cache takes tokens of {' or '.join(map(str, self._c))}, got {dtype}")
-        return self._c[dtype]
+        return c
 
-    def _workspace(self, q, s: SageKvSeqs, p: SageDecodeParams, args) -> torch.Tensor:
+    def _workspace(self, q, sizes, args) -> torch.Tensor:
         """A workspace for a decode of these sizes (the number of bytes goes by them alone)."""
-        key = s.B, s.max_pages, p.Hq, p.window, p.sinks
-        n = self._ws_bytes.get(key)
+        n = self._ws_bytes.get(sizes)
         if n is None:
-            n = self._ws_bytes[key] = int(lib().sage_decode_workspace_bytes(*args))
+            n = self._ws_bytes[sizes] = int(lib().sage_decode_workspace_bytes(*args))
         if n <= 256:  # nothing is kept there: any place will do
             return self._no_workspace
         return q.new_empty((n,), dtype=torch.uint8)
@@ -602,29 +602,31 @@ def decode_workspace_bytes(cache: KVCache, page_table, lens, Hq: int, *, window:
 def _decode(q, cache, page_table, lens, window, sinks, sm_scale, km, out, lse, want_lse, workspace, stream):
     _range32("window, sinks", window, sinks)
     c, s = cache._struct(q.dtype), cache._seqs(page_table, lens)
+    B, max_pages = page_table.shape
     Hq = q.shape[1] if q.dim() == 3 else 0
-    _expect("q", q, (s.B, Hq, cache.d), q.dtype)
+    _expect("q", q, (B, Hq, cache.d), q.dtype)
     if Hq < 1 or Hq % cache.Hkv:
         raise ValueError(f"query heads must be a multiple of {cache.Hkv}, got {Hq}")
+    index = _one_device("cache, q, page_table, lens", cache._index, q, page_table, lens)
     if out is not None:
         _expect("out", out, q.shape, q.dtype)
     if lse is not None:
-        _expect("lse", lse, (s.B, Hq), torch.float32)
+        _expect("lse", lse, (B, Hq), torch.float32)
     if km is not None:
         if not cache.quantized:
             raise ValueError("km goes with a quantized cache")
-        _expect("km", km, (s.B, cache.Hkv, cache.d), torch.float32)
+        _expect("km", km, (B, cache.Hkv, cache.d), torch.float32)
     if workspace is not None:
         _expect("workspace", workspace, (workspace.numel(),), torch.uint8)
-    index = _one_device("cache, q, page_table, lens, km, out, lse, workspace", cache._index, q, page_table, lens, km,
-                        out, lse, workspace)
+    if not (out is lse is km is workspace is None):
+        _one_device("cache, km, out, lse, workspace", index, km, out, lse, workspace)
     p = SageDecodeParams(Hq, window, sinks, float(sm_scale if sm_scale else 0.0))
     args = ctypes.byref(c), ctypes.byref(s), ctypes.byref(p)
 
     def work(raw):
         o = torch.empty_like(q) if out is None else out
-        z = q.new_empty((s.B, Hq), dtype=torch.float32) if lse is None and want_lse else lse
-        ws = cache._workspace(q, s, p, args) if workspace is None else workspace
+        z = q.new_empty((B, Hq), dtype=torch.float32) if lse is None and want_lse else lse
+        ws = cache._workspace(q, (B, max_pages, Hq, window, sinks), args) if workspace is None else workspace
         _check(lib().sage_attn_decode(q.data_ptr(), o.data_ptr(), _ptr(z), _ptr(km), *args, ws.data_ptr(), ws.numel(),
                                       raw), "sage_attn_decode")
         return o, z
