@@ -476,8 +476,11 @@ SAGE_API size_t sage_decode_workspace_bytes(const sage_kv_cache *c, const sage_k
  * before km was taken off.  With c->weight, every visible key's weight grows by
  * sum over the query heads of its group of exp(S_j - lse); sequences of one call,
  * and of calls that run at the same time, must not share pages then.
- * Softmax statistics and sums are held in fp32; the weights of V enter the
- * tensor cores as two 16-bit numbers that together carry 16 bits or more.
+ * Softmax statistics and sums are held in fp32.  The weights of V enter the
+ * tensor cores as two 16-bit numbers that together carry 16 bits or more; in
+ * fp16 (fp16 caches; quantised ones, where a weight is taken times v_scale) this
+ * holds down to 2^-21 of the heaviest weight (of the largest v_scale), and what
+ * lies below 2^-38 of it may count as 0 for o.
  * Results do not depend on scheduling (no atomics): the same inputs give the
  * same bytes.
  */

@@ -236,6 +236,9 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
   constexpr int kRowsPerLoad = 32 / kChunks;
   constexpr int NT = D / 8;                        // n-tiles of O
   constexpr bool kVB = CT == kBF16;                // V and the weights as bf16
+  // fp16 weights (at most 1) are held in units of 2^-15: fp16 ends at 2^-24, and a weight of 2^-25 beside a heavy key
+  // would be lost from O and kept in l.  (bf16 has fp32's range, and the 8-bit path a unit of its own, v_unit.)
+  constexpr float kUnit = CT == kFP16 ? 32768.0f : 1.0f;
   constexpr int E = CT == kQ8 ? 1 : 2;             // bytes of an element
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ long long s_sum[kDecWarps];
@@ -608,6 +611,9 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
           if constexpr (CT == kQ8) {
             x *= vs[t][0];
             y *= vs[t][1];
+          } else {
+            x *= kUnit;
+            y *= kUnit;
           }
           split_pair<kVB>(x, y, hi[2 * t + half], lo[2 * t + half]);
         }
@@ -677,6 +683,9 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeArgs a)
         if constexpr (CT == kQ8) {
           x0 *= __uint_as_float((uint32_t)(127 - 14 + v_exp) << 23);
           x1 *= __uint_as_float((uint32_t)(127 - 14 + v_exp) << 23);
+        } else {
+          x0 *= 1.0f / kUnit;
+          x1 *= 1.0f / kUnit;
         }
         if constexpr (CT != kQ8) {
           so[r * D + n * 8 + 2 * (lane & 3)] = x0;

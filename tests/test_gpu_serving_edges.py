@@ -1,0 +1,59 @@
+"""Serving operators on the GPU at the edges of their number formats and of what
+their inputs may hold.  References in 64 bits; tolerances are counted in the test."""
+import math
+
+import pytest
+import torch
+
+from quantized_attention_block_b200 import sage
+
+from serving_ref import HALF_STEP, score_error
+from test_gpu_serving import no_device_error  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+BF, FP = torch.bfloat16, torch.float16
+LN2 = math.log(2.0)
+
+
+# ---------------------------------------------------------------- light keys beside a heavy one
+@pytest.mark.parametrize("G", [4, 12])
+@pytest.mark.parametrize("d,dtype", [(64, FP), (128, FP), (64, BF)])
+@pytest.mark.parametrize("B,H,n", [(37, 8, 2048), (1, 1, 8192)])
+def test_decode_keeps_light_keys_beside_heavy_ones(B, H, n, d, dtype, G):
+    """A heavy key with V = 0 in the first block of each warp, the others 2^-25 as heavy: all of the output comes from
+    them.  Rows that one CTA does alone (128 blocks), and a split one (shares of 8 blocks)."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    per = n // 16
+    t = -25.0 + torch.randint(-32, 33, (B, H, n), generator=g, device="cuda") / 64.0
+    v = 512.0 + 1024.0 * torch.rand((B, H, n, d), generator=g, device="cuda")
+    at = torch.arange(per, device="cuda")
+    heavy = (at[at % 8 < 4] if B == 1 else at[:4]) * 16
+    t[..., heavy], v[..., heavy, :] = 0.0, 0.0
+    if dtype == BF:
+        t = t.round()  # (bf16 holds eight bits of a score)
+    k = torch.zeros((B, H, n, d), device="cuda")
+    k[..., 0] = t
+    k, v = k.to(dtype), v.to(dtype)
+    q = torch.randn((B, H * G, d), generator=g, device="cuda").to(dtype)
+    q[..., 0] = 1.0
+
+    def pages(x):
+        return x.view(B, H, per, 16, d).transpose(1, 2).reshape(B * per, H, 16, d).contiguous()
+
+    cache = sage.KVCache(pages(k), pages(v))
+    table = torch.arange(B * per, dtype=torch.int32, device="cuda").view(B, per)
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    got, lse = sage.sage_attn_decode_lse(q, cache, table, lens, sm_scale=LN2)
+    p = torch.exp2(t.double())
+    l = p.sum(-1, keepdim=True)
+    ref = ((p / l)[..., None] * v.double()).sum(2)[:, :, None].expand(-1, -1, G, -1).reshape(B, H * G, d)
+    # Scores off by err move a weight by a factor e^(+-2 err), here of an output without the heavy key's V; the two
+    # 16-bit parts of a weight carry 16 bits, or (fp16, which ends at 2^-24) half of 2^-24 x 2^-15 of the warp's
+    # heaviest; exponentials 2^-22; a warp and turn rounds its sum once (or truncates: 2^-23), then pieces are joined.
+    err = score_error(torch.ones(1, 1), torch.full((1, 1), 26.0), LN2) + 2.0 ** -22
+    rel = 4 * err + 2.0 ** -16 + 2.0 ** -22 + (n / 64 + 600) * 2.0 ** -23
+    tol = (HALF_STEP[dtype] + rel) * ref + n * 2.0 ** -40 / l[..., 0].min().item() * v.abs().max().item() + 2.0 ** -25
+    assert (ref > 2.0 ** -14).all()
+    assert ((got.double() - ref).abs() <= tol).all(), ((got.double() / ref).min().item(), (got.double() / ref).max().item())
+    want = torch.log(l[..., 0])[:, :, None].expand(-1, -1, G).reshape(B, H * G)
+    assert ((lse.double() - want).abs() <= err + 2.0 ** -21 * (4 + want.abs())).all()
