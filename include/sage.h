@@ -520,6 +520,9 @@ typedef struct {
 /*
  * Sliding-window attention with sinks over whole sequences (the local layers
  * of a model), in the inputs' 16-bit type, with fp32 sums and softmax.
+ * The weights enter P V rounded once to the inputs' type (half a step: bf16
+ * 2^-8 relative, fp16 2^-11, or 2^-32 of the heaviest if that is more); l and
+ * lse take them unrounded.
  * q, k, v, o: device, contiguous, in the layout of p.  lse: device fp32
  * [B, Hq, N] or NULL.  lens: device [B] or NULL (N for every sequence): rows
  * i >= lens[b] of o and lse are left as they are (p->zero_tail: set to zero) and

@@ -57,13 +57,17 @@ namespace {
 
 constexpr int kWinThreads = 512;
 constexpr int kStep = 64;              // keys of a step; rows of a half key tile (few sinks)
-constexpr float kWinSlack = 8.0f;      // log2 of the largest weight before O is rescaled
+constexpr float kWinSlack = 8.0f;      // log2 of the largest weight over that of m, before O is rescaled
+// log2 of m's own weight.  P has 16 bits; fp16 ends at 2^-24 and at 2^16, so the weights go up to 2^(8 + 7), and what a
+// key loses there is at most 2^-32 of the heaviest (without the 7, 2^-25: keys 2^-24.5 as heavy came out 41% heavier).
+template <typename T>
+constexpr float kWinLift = std::is_same<T, __half>::value ? 7.0f : 0.0f;
 template <int D>
 struct WinSmem {
   static constexpr uint32_t kTileBytes = 128 * D * 2;
   static constexpr int kRing = D == 128 ? 5 : 8;  // K and V tiles in turn
   static constexpr uint32_t oRing = 2 * kTileBytes;
-  static constexpr uint32_t oL = oRing + kRing * kTileBytes;  // float2[2][128]: l, sm_scale log2(e) m
+  static constexpr uint32_t oL = oRing + kRing * kTileBytes;  // float2[2][128]: l, sm_scale log2(e) m - kWinLift
   static constexpr uint32_t oItem = oL + 2 * 128 * 8;         // WinItem[2], then the launch queue's answer
   static constexpr uint32_t oBar = oItem + 2 * 32 + 16;
   static constexpr uint32_t kBars = 2 * kRing + 1 + 2 * 13;
@@ -611,7 +615,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
             tmem_st16p(tO + x, o);
           }
         }
-        const float ms = m == -INFINITY ? 0.0f : m * scale;
+        const float ms = (m == -INFINITY ? 0.0f : m * scale) - kWinLift<T>;
         const float2 sc = make_float2(scale, scale), off = make_float2(-ms, -ms);
         float2 sum[4] = {};
 #pragma unroll
@@ -622,7 +626,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
             const float2 u = ffma2(make_float2(__uint_as_float(s[x + e]), __uint_as_float(s[x + e + 1])), sc, off);
             const float2 f = make_float2(ex2_approx(u.x), ex2_approx(u.y));
             sum[(e / 2) & 3] = fadd2(sum[(e / 2) & 3], f);
-            y[e / 2] = pack16<T>(f.x, f.y);
+            y[e / 2] = pack16<T>(f.x, f.y);  // A of P V has V's type: one rounding, after the sum has taken f
           }
           tmem_st16p(tS + x / 2, y);
         }
@@ -636,7 +640,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       if (!ok) break;
       // l and m for the output warps, once they have read the last item's
       if (n_items > 0 && !(ok = mbar_wait_warp(&bar.o_free[ti], (n_items - 1) & 1))) break;
-      s_l[128 * ti + row] = make_float2(l, m * scale);
+      s_l[128 * ti + row] = make_float2(l, m * scale - kWinLift<T>);
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.l_ready[ti]);
       ++n_items;

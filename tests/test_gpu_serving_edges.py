@@ -57,3 +57,34 @@ def test_decode_keeps_light_keys_beside_heavy_ones(B, H, n, d, dtype, G):
     assert ((got.double() - ref).abs() <= tol).all(), ((got.double() / ref).min().item(), (got.double() / ref).max().item())
     want = torch.log(l[..., 0])[:, :, None].expand(-1, -1, G).reshape(B, H * G)
     assert ((lse.double() - want).abs() <= err + 2.0 ** -21 * (4 + want.abs())).all()
+
+
+@pytest.mark.parametrize("window", [0, 900])
+@pytest.mark.parametrize("d,dtype", [(64, FP), (128, FP), (128, BF)])
+def test_window_keeps_light_keys_beside_a_heavy_one(window, d, dtype):
+    """Key 0 (a sink) with V = 0, the others 2^-24.5 as heavy: fp16 ends at 2^-24 of what a weight is a part of."""
+    N, light = 1500, -24.5
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k = torch.zeros((1, 1, N, d), device="cuda")
+    k[..., 0] = light
+    k[..., 0, 0] = 0.0
+    v = 512.0 + 1024.0 * torch.rand((1, 1, N, d), generator=g, device="cuda")
+    v[..., 0, :] = 0.0
+    q = torch.randn((1, 1, N, d), generator=g, device="cuda")
+    q[..., 0] = 1.0
+    q, k, v = q.to(dtype), k.to(dtype), v.to(dtype)
+    got, lse = sage.sage_attn_window_fwd_lse(q, k, v, window=window, sinks=1, sm_scale=LN2)
+    i = torch.arange(N, device="cuda")
+    see = (i[None] <= i[:, None]) & ((i[:, None] - i[None] < window) | (i[None] < 1) | (window == 0))
+    p = torch.exp2(k[0, 0, :, 0].double()) * see
+    l = p.sum(-1, keepdim=True)
+    ref = (p / l) @ v[0, 0].double()
+    # The weights in the inputs' type: half a step, and as much again for their sum (taken before that rounding); in
+    # fp16 at least half of 2^-24, in units of at most 2^-7 of the heaviest.  The rest as above; steps of 64 keys are
+    # four products of 16.
+    err = score_error(torch.ones(1, 1), torch.full((1, 1), 25.0), LN2) + 2.0 ** -22
+    rel = 3 * HALF_STEP[dtype] + 4 * err + 2.0 ** -21 + (N / 16 + 8) * 2.0 ** -23
+    tol = rel * ref + 2.0 ** -25 + (N * 2.0 ** -32 * v.abs().max().item() if dtype == FP else 0.0)
+    got = got[0, 0].double()
+    assert ((got - ref).abs() <= tol).all(), (got[-1] / ref[-1]).mean().item()
+    assert ((lse[0, 0].double() - torch.log(l[:, 0])).abs() <= err + 2.0 ** -21 * (4 + torch.log(l[:, 0]).abs())).all()
