@@ -527,7 +527,9 @@ typedef struct {
  * [B, Hq, N] or NULL.  lens: device [B] or NULL (N for every sequence): rows
  * i >= lens[b] of o and lse are left as they are (p->zero_tail: set to zero) and
  * of k, v are not used (values outside [0, N] are taken as the nearest bound).  A key that a row does
- * not see has no influence on that row, whatever it holds.
+ * not see has no influence on that row, whatever it holds.  An infinity in the v of a key that it sees gives an
+ * infinity in that channel, or NaN if the key's weight rounds to zero.  Rows that saw a step of keys with a NaN or
+ * an infinity in the v of one that they do not see are computed twice, the second time a row a warp: right, and slow.
  */
 SAGE_API sage_status sage_attn_window_fwd(const void *q, const void *k, const void *v, void *o, float *lse,
                                           const int32_t *lens, const sage_window_params *p, void *stream);

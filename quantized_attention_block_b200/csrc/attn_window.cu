@@ -39,9 +39,13 @@
 //
 // Keys a row does not see are -inf before the maximum, so their weights are
 // exact zeros; a NaN or infinity in such a key's V still makes 0 x inf = NaN in
-// the product, so a row whose output is not finite is computed again over its
-// visible keys alone (window_row).  Rows of V behind a sequence's end (padding,
-// which may hold anything) are zeroed in shared memory first.
+// the product.  A row whose output is not finite is noted, and once the CTA's
+// last item is done (its waits are over, so this may take any time) it is
+// computed again over its visible keys alone (window_row) if one of its steps
+// held such a key.  A CTA with a row to do again takes no more items, so that
+// its notes stay few; the hardware starts the others on CTAs of their own.  Rows
+// of V behind a sequence's end (padding, which may hold anything) are zeroed in
+// shared memory first.
 #include <climits>
 #include <type_traits>
 
@@ -62,6 +66,9 @@ constexpr float kWinSlack = 8.0f;      // log2 of the largest weight over that o
 // key loses there is at most 2^-32 of the heaviest (without the 7, 2^-25: keys 2^-24.5 as heavy came out 41% heavier).
 template <typename T>
 constexpr float kWinLift = std::is_same<T, __half>::value ? 7.0f : 0.0f;
+// Items of which an output warp may have rows to do again: the first, and the three that may be on their way by then
+// (the ring of items holds two, and the one behind them is asked for before they are read)
+constexpr int kAgain = 4;
 template <int D>
 struct WinSmem {
   static constexpr uint32_t kTileBytes = 128 * D * 2;
@@ -69,7 +76,8 @@ struct WinSmem {
   static constexpr uint32_t oRing = 2 * kTileBytes;
   static constexpr uint32_t oL = oRing + kRing * kTileBytes;  // float2[2][128]: l, sm_scale log2(e) m - kWinLift
   static constexpr uint32_t oItem = oL + 2 * 128 * 8;         // WinItem[2], then the launch queue's answer
-  static constexpr uint32_t oBar = oItem + 2 * 32 + 16;
+  static constexpr uint32_t oAgain = oItem + 2 * 32 + 16;     // WinAgain[4][kAgain], then their numbers
+  static constexpr uint32_t oBar = oAgain + 4 * kAgain * 16 + 16;
   static constexpr uint32_t kBars = 2 * kRing + 1 + 2 * 13;
   static constexpr uint32_t oTmem = oBar + 8 * kBars;
   static constexpr uint32_t kBytes = oTmem + 16;
@@ -100,17 +108,39 @@ struct WinSteps {
 __device__ __forceinline__ int win_key(const WinItem& w, int u) {  // first key of a step
   return kStep * u + (u >= 2 * w.ns ? 128 * (w.t0 - w.ns) : 0);
 }
+// Which steps of the row tile at p0 hold keys that one of its rows does not see: from `diagonal` on, keys behind its
+// first row; before `whole`, keys that its last row's window leaves out, unless the step is one of the first
+// `whole_sinks`
+struct WinMask {
+  int diagonal, whole_sinks, whole;
+  __device__ __forceinline__ WinMask(const WindowArgs& a, const WinItem& w, int p0) {
+    const int out = p0 + 128 - a.window - 128 * (w.t0 - w.ns);
+    diagonal = 2 * (w.ns + p0 / 128 - w.t0);
+    whole_sinks = a.sinks / kStep;
+    whole = a.window > 0 && p0 + 128 > a.window ? (out + kStep - 1) / kStep : 0;
+  }
+  __device__ __forceinline__ bool operator()(int u) const { return u >= diagonal || (u >= whole_sinks && u < whole); }
+};
+// the low n bits (n taken as the nearest of 0 and 32)
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+// which of the keys key0 + 32 x + 0..31 row p sees: columns c <= hi and (c >= lo or c < sk) of the step
+__device__ __forceinline__ uint32_t win_sees(const WindowArgs& a, int p, int key0, int x) {
+  const int hi = p - key0, lo = a.window > 0 ? hi - a.window + 1 : INT_MIN, sk = a.sinks - key0;
+  return low_bits(hi + 1 - 32 * x) & (~low_bits(lo - 32 * x) | low_bits(sk - 32 * x));
+}
+// Rows to do again, of a warp's quarter of an item's row tiles
+struct __align__(16) WinAgain {
+  int bh, q0;
+  uint32_t rows[2];
+};
 static_assert(sizeof(WinItem) == 32, "items are passed through shared memory as two 16-byte words");
 
-__device__ __forceinline__ WinItem win_item(const WindowArgs& a, uint32_t idx) {
-  // heads in groups whose K and V stay in L2 while every pair of their rows runs, heaviest rows first
+// rows q0.. of head bh = b Hq + h
+__device__ __forceinline__ WinItem win_rows(const WindowArgs& a, uint32_t bh, int q0) {
   WinItem w;
-  const uint32_t per = a.group * a.pairs, g = idx / per, in = idx - g * per;
-  const uint32_t heads = min((uint32_t)a.group, (uint32_t)(a.B * a.Hq) - g * a.group);
-  const uint32_t pair = in / heads, bh = g * a.group + in - pair * heads;
   w.b = bh / a.Hq;
   w.h = bh - w.b * a.Hq;
-  w.q0 = 256 * (a.pairs - 1 - (int)pair);
+  w.q0 = q0;
   w.n = a.lens ? min(max(__ldg(a.lens + w.b), 0), a.N) : a.N;
   const int lead = w.q0 - a.window + 1;
   w.t0 = a.window > 0 && lead > 0 ? lead / 128 : 0;
@@ -119,6 +149,13 @@ __device__ __forceinline__ WinItem win_item(const WindowArgs& a, uint32_t idx) {
   w.nt = w.q0 >= w.n ? 0 : w.ns + w.q0 / 128 - w.t0 + (w.q0 + 128 < w.n ? 2 : 1);
   w.narrow = w.ns > 0 && a.sinks - 128 * (w.ns - 1) <= kStep ? w.ns - 1 : -1;
   return w;
+}
+__device__ __forceinline__ WinItem win_item(const WindowArgs& a, uint32_t idx) {
+  // heads in groups whose K and V stay in L2 while every pair of their rows runs, heaviest rows first
+  const uint32_t per = a.group * a.pairs, g = idx / per, in = idx - g * per;
+  const uint32_t heads = min((uint32_t)a.group, (uint32_t)(a.B * a.Hq) - g * a.group);
+  const uint32_t pair = in / heads, bh = g * a.group + in - pair * heads;
+  return win_rows(a, bh, 256 * (a.pairs - 1 - (int)pair));
 }
 
 // One row by one warp, over its visible keys alone: lane = key for the scores,
@@ -191,6 +228,46 @@ __device__ __forceinline__ void window_row(const WindowArgs& a, int b, int hq, i
   if (a.lse && lane == 0) a.lse[((int64_t)b * a.Hq + hq) * a.N + i] = (m + log2f(l)) * 0.6931471805599453f;
 }
 
+// Of 32 rows of row tile i of an item, computes those of `rows` again whose steps held a NaN or an infinity in the V of
+// a key that the row does not see; lane = row.  (What a row does see reached its output as it should.)
+template <typename T, int D>
+__device__ __forceinline__ void window_again(const WindowArgs& a, const WinItem& w, int i, int quarter, uint32_t rows) {
+  constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+  constexpr int LR = D / 8, RP = 32 / LR;  // lanes of a row of V, rows of a load
+  const int lane = threadIdx.x & 31, hk = w.h / (a.Hq / a.Hkv);
+  const int p0 = w.q0 + 128 * i, first = p0 + 32 * quarter;
+  const WinSteps st(a, w, i);
+  const WinMask masked(a, w, p0);
+  bool again = false;
+  for (int u = st.first; u != st.end; u = st.next(u)) {
+    if (!masked(u)) continue;
+    const int key0 = win_key(w, u);
+#pragma unroll 1
+    for (int x = 0; x < kStep / 32; ++x) {
+      uint32_t bad = 0;  // of 32 keys
+#pragma unroll 8
+      for (int r = 0; r < 32; r += RP) {
+        const int j = key0 + 32 * x + r + lane / LR;
+        uint4 z = make_uint4(0, 0, 0, 0);  // (behind the end: zeroed before the product)
+        if (j < w.n)
+          z = reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) +
+                                             row_offset((int64_t)w.b * a.Hkv + hk, j, a.Hkv, a.N, D, a.nhd))[lane % LR];
+        const uint32_t y[4] = {z.x, z.y, z.z, z.w};
+        bool odd = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) odd |= (y[e] & kExp) == kExp || (y[e] >> 16 & kExp) == kExp;
+        const uint32_t all = __ballot_sync(0xffffffffu, odd);
+#pragma unroll
+        for (int g = 0; g < RP; ++g)
+          if (all >> (g * LR) & ((1u << LR) - 1u)) bad |= 1u << (r + g);
+      }
+      again |= (bad & ~win_sees(a, first + lane, key0, x)) != 0;
+    }
+  }
+  for (rows &= __ballot_sync(0xffffffffu, again); rows; rows &= rows - 1)
+    window_row<T, D>(a, w.b, w.h, first + __ffs(rows) - 1);
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack16(float x, float y);
 template <>
@@ -203,9 +280,6 @@ __device__ __forceinline__ uint32_t pack16<__half>(float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-
-// the low n bits (n taken as the nearest of 0 and 32)
-__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
 __device__ __forceinline__ void store_row32(void* p, const uint32_t* w, bool wide) {
   if (wide)
@@ -273,6 +347,8 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   uint8_t* ring = smem_win + L::oRing;
   float2* s_l = reinterpret_cast<float2*>(smem_win + L::oL);
   WinItem* items = reinterpret_cast<WinItem*>(smem_win + L::oItem);
+  WinAgain* again = reinterpret_cast<WinAgain*>(smem_win + L::oAgain);  // [4][kAgain]: a list an output warp
+  volatile uint32_t* n_again = reinterpret_cast<uint32_t*>(again + 4 * kAgain);
   WinBars bar;
   bar.kv_full = reinterpret_cast<uint64_t*>(smem_win + L::oBar);
   bar.kv_empty = bar.kv_full + R;
@@ -293,6 +369,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_win + L::oTmem);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, wg = warp / 4;
+  if (threadIdx.x < 4) n_again[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < R; ++s) {
       mbar_init(&bar.kv_full[s], 1);
@@ -519,7 +596,9 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       bool have = true;  // idx is an item
       auto ask = [&] {
         bool got = false;
-        if (lane == 0) {
+        // (no more items with a row to do again: by the time that an output warp reads the item after one, the third
+        // item after it may have been asked for, and the wait to post that one shows the note here)
+        if (lane == 0 && !(n_again[0] | n_again[1] | n_again[2] | n_again[3])) {
           mbar_expect_tx(bar.answer, 16);
           clc_try_cancel(items + 2, bar.answer);
           got = mbar_wait(bar.answer, asked & 1) && clc_answer(items + 2, idx);
@@ -563,27 +642,20 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       if (st.end == 0) continue;
       const int p0 = w.q0 + 128 * ti, p = p0 + row;
       float m = -INFINITY, l = 0.0f;
-      // steps from `diagonal` on hold keys behind the tile's first row; before `whole`, keys that its last row's
-      // window leaves out, unless the step is one of the first `whole_sinks`
-      const int diagonal = 2 * (w.ns + p0 / 128 - w.t0), whole_sinks = a.sinks / kStep;
-      const int out = p0 + 128 - a.window - 128 * (w.t0 - w.ns);
-      const int whole = a.window > 0 && p0 + 128 > a.window ? (out + kStep - 1) / kStep : 0;
+      const WinMask masked(a, w, p0);
       for (int u = st.first; u != st.end; u = st.next(u), ++step) {
         const uint32_t tS = tmem + 128 * ti + 64 * (step & 1) + lanes;
-        // keys behind the first row's position, or before the last row's window and not all sinks
-        const bool masked = u >= diagonal || (u >= whole_sinks && u < whole);
         if (!(ok = mbar_wait_warp(&bar.s_full[2 * ti + (step & 1)], (step >> 1) & 1))) break;
         tc_fence_after();
         uint32_t s[kStep];
         tmem_ld32p(tS, s);
         tmem_ld32p(tS + 32, s + 32);
         tmem_ld_wait();
-        if (masked) {
-          // columns c <= hi and (c >= lo or c < sk) are visible
-          const int key0 = win_key(w, u), hi = p - key0, lo = a.window > 0 ? hi - a.window + 1 : INT_MIN, sk = a.sinks - key0;
+        if (masked(u)) {
+          const int key0 = win_key(w, u);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const uint32_t see = low_bits(hi + 1 - 32 * x) & (~low_bits(lo - 32 * x) | low_bits(sk - 32 * x));
+            const uint32_t see = win_sees(a, p, key0, x);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (!((see >> e) & 1)) s[32 * x + e] = __float_as_uint(-INFINITY);
@@ -649,10 +721,11 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     // ------------------------------------------------------------ output
     const int quarter = warp & 3, row = quarter * 32 + lane;
     const bool wide = (reinterpret_cast<uintptr_t>(a.o) & 31) == 0;
-    uint32_t n_items[2] = {0, 0};
+    uint32_t n_items[2] = {0, 0}, noted = 0;
     bool ok = true;
     WinItem w;
     for (uint32_t nth = 0; ok && win_next(items, bar, nth, w); ++nth) {
+      uint32_t redo[2] = {0, 0};
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int p = w.q0 + 128 * i + row;
@@ -696,8 +769,14 @@ __global__ void __launch_bounds__(kWinThreads, 1)
           }
         }
         if (a.lse && p < w.n) a.lse[head * a.N + p] = (lm.y + log2f(lm.x)) * 0.6931471805599453f;
-        uint32_t redo = __ballot_sync(0xffffffffu, odd != 0.0f && p < w.n);
-        for (; redo; redo &= redo - 1) window_row<T, D>(a, w.b, w.h, w.q0 + 128 * i + quarter * 32 + __ffs(redo) - 1);
+        redo[i] = __ballot_sync(0xffffffffu, odd != 0.0f && p < w.n);
+      }
+      if (redo[0] | redo[1]) {
+        if (lane == 0) {
+          again[kAgain * quarter + noted] = {w.b * a.Hq + w.h, w.q0, {redo[0], redo[1]}};
+          n_again[quarter] = noted + 1;
+        }
+        ++noted;
       }
     }
   }
@@ -708,6 +787,14 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   if (warp == 13) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
+  }
+  // rows to do again: (item, row tile, quarter) in turn to the warps
+  for (int x = warp; x < 8 * kAgain; x += kWinThreads / 32) {
+    const int quarter = x % 4, i = x / 4 % 2, nth = x / 8;
+    if (nth >= n_again[quarter]) continue;
+    const WinAgain& r = again[kAgain * quarter + nth];
+    const uint32_t rows = r.rows[i];
+    if (rows) window_again<T, D>(a, win_rows(a, r.bh, r.q0), i, quarter, rows);
   }
 }
 

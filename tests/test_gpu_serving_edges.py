@@ -7,7 +7,7 @@ import torch
 
 from quantized_attention_block_b200 import sage
 
-from serving_ref import HALF_STEP, score_error
+from serving_ref import HALF_STEP, assert_within, out_tol, score_error
 from test_gpu_serving import no_device_error  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -88,3 +88,86 @@ def test_window_keeps_light_keys_beside_a_heavy_one(window, d, dtype):
     got = got[0, 0].double()
     assert ((got - ref).abs() <= tol).all(), (got[-1] / ref[-1]).mean().item()
     assert ((lse[0, 0].double() - torch.log(l[:, 0])).abs() <= err + 2.0 ** -21 * (4 + torch.log(l[:, 0]).abs())).all()
+
+
+# ---------------------------------------------------------------- NaN and infinity in V, in many items
+@pytest.fixture
+def short_waits():
+    """Waits inside the kernels give up after 20 ms; what they wait for here takes microseconds."""
+    sage.sage_debug_wait_limit(20000)
+    yield
+    torch.cuda.synchronize()
+    sage.sage_debug_wait_limit(0)
+
+
+def some_rows(q, k, v, b, h, rows, window, sinks):
+    """(o, tolerance) of some rows of a head in 64 bits, over their visible keys alone."""
+    hk = h // (q.shape[1] // k.shape[1])
+    qq, kk = q[b, h, rows].double().cpu(), k[b, hk].double().cpu()
+    scale = 1.0 / math.sqrt(q.shape[-1])
+    o, tol = [], []
+    for x, i in zip(qq, rows.tolist()):
+        j = torch.arange(i + 1)
+        j = j if window == 0 else j[(i - j < window) | (j < sinks)]
+        vv = v[b, hk, j].double().cpu()
+        w = torch.softmax(kk[j] @ x * scale, 0)
+        o.append(w @ vv)
+        # as in serving_ref.window_ref
+        finite = torch.nan_to_num(vv, nan=0.0, posinf=0.0, neginf=0.0).abs()
+        tol.append(out_tol(o[-1], finite, score_error(x[None], kk[j], scale), q.dtype)
+                   + 2 * HALF_STEP[q.dtype] * (w @ finite))
+    return torch.stack(o), torch.stack(tol)
+
+
+def many_items(N, d, dtype, H, Hkv):
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q, k, v = (torch.randn((1, h, N, d), generator=g, device="cuda").to(dtype) for h in (H, Hkv, Hkv))
+    return q, k, v
+
+
+@pytest.mark.parametrize("d,dtype,window", [(128, BF, 0), (64, FP, 0), (128, FP, 300)])
+def test_window_a_visible_infinity_reaches_its_channel_alone(short_waits, d, dtype, window):
+    """An infinity in the V of key 0, which every row sees: seven items a CTA, none of which is held up."""
+    q, k, v = many_items(8192, d, dtype, 32, 8)
+    want, want_lse = sage.sage_attn_window_fwd_lse(q, k, v, window=window, sinks=1)
+    v[:, :, 0, 3] = math.inf
+    got, lse = sage.sage_attn_window_fwd_lse(q, k, v, window=window, sinks=1)
+    torch.cuda.synchronize()
+    assert sage.sage_last_device_error() == 0
+    assert (got[..., 3] == math.inf).all()
+    keep = [c for c in range(d) if c != 3]
+    assert torch.equal(got[..., keep], want[..., keep]) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("d,dtype", [(128, BF), (64, FP)])
+def test_window_a_late_nan_leaves_the_rows_before_it(short_waits, d, dtype):
+    q, k, v = many_items(8192, d, dtype, 32, 8)
+    want = sage.sage_attn_window_fwd(q, k, v, window=0)
+    v[:, :, 5000, 3] = math.nan
+    got = sage.sage_attn_window_fwd(q, k, v, window=0)
+    torch.cuda.synchronize()
+    assert sage.sage_last_device_error() == 0
+    assert torch.equal(got[:, :, :4992], want[:, :, :4992])  # row tiles that do not reach key 5000
+    keep = [c for c in range(d) if c != 3]
+    assert torch.equal(got[:, :, 5000:][..., keep], want[:, :, 5000:][..., keep])
+    assert torch.isnan(got[:, :, 5000:, 3]).all()
+    for h in (0, 13, 31):
+        ref, tol = some_rows(q, k, v, 0, h, torch.arange(4992, 5000), 0, 0)
+        assert_within(got[0, h, 4992:5000], ref, tol)
+
+
+@pytest.mark.parametrize("d,dtype,window,sinks", [(128, BF, 0, 0), (64, FP, 700, 70)])
+def test_window_nan_in_every_value_of_a_channel(short_waits, d, dtype, window, sinks):
+    """Nearly every row is computed again: thousands of them, none within a wait of another role."""
+    q, k, v = many_items(4096, d, dtype, 32, 32)
+    v[..., 3] = math.nan
+    got = sage.sage_attn_window_fwd(q, k, v, window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    assert sage.sage_last_device_error() == 0
+    assert torch.isnan(got[..., 3]).all()
+    keep = [c for c in range(d) if c != 3]
+    assert torch.isfinite(got[..., keep]).all()
+    rows = torch.tensor([0, 1, 63, 127, 128, 700, 1999, 2048, 3333, 4095])
+    for h in (0, 17, 31):
+        ref, tol = some_rows(q, k, v, 0, h, rows, window, sinks)
+        assert_within(got[0, h, rows][..., keep], ref[:, keep], tol[:, keep])
