@@ -273,6 +273,8 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const EvictArgs 
 // has its 16 bytes of K and V of two rows in flight.  More are slower, not faster
 // (192 us in all with two, 246 with four, 321 with eight for 128 rows of up to
 // 12288 tokens), and so are accesses that stay in L2 (212 us).
+// (kept with plain loads: the selection may still write it when this kernel
+// starts, and the non-coherent ones are for data that no kernel writes meanwhile.)
 constexpr int kMoveThreads = 128, kMoveRows = 2;
 
 template <int ROW_BYTES>
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictArgs a
   constexpr int ROWS = PASS * kMoveRows;  // of the CTA at a time
   static_assert(ROWS <= kMoveThreads, "a thread a row");
   for (int i = blockIdx.y * ROWS + threadIdx.x; threadIdx.x < ROWS && i < n; i += gridDim.y * ROWS) {
-    const int j = __ldg(a.kept + (int64_t)bh * a.keep + i);
+    const int j = a.kept[(int64_t)bh * a.keep + i];
     const int sp = __ldg(a.c.table + (int64_t)b * a.c.max_pages + (j >> a.c.page_log2));
     const int dp = __ldg(a.dst_table + (int64_t)b * a.dst_pages + (i >> a.c.page_log2));
     if ((uint32_t)sp >= (uint32_t)a.c.n_pages || (uint32_t)dp >= (uint32_t)a.c.n_pages) continue;
@@ -310,7 +312,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictArgs a
 #pragma unroll
     for (int x = 0; x < kMoveRows; ++x) {
       const int i = i0 + x * PASS;
-      j[x] = i < n ? __ldg(a.kept + (int64_t)bh * a.keep + i) : -1;
+      j[x] = i < n ? a.kept[(int64_t)bh * a.keep + i] : -1;
       dp[x] = i < n ? __ldg(a.dst_table + (int64_t)b * a.dst_pages + (i >> a.c.page_log2)) : 0;
     }
 #pragma unroll
