@@ -193,9 +193,10 @@ SAGE_API sage_status sage_debug_qk_int32(const sage_quant_view *view, const sage
                                 int32_t *out_128x128, void *stream);
 
 /*
- * Returns the device-side error recorded since the last call and clears it:
- * SAGE_OK, SAGE_ERR_TIMEOUT, or (no wait gave up) SAGE_ERR_BAD_PAGE from the
- * paged-cache entry points.  Synchronises `stream`.
+ * Returns a device-side error recorded since the last call and clears it:
+ * SAGE_ERR_TIMEOUT, else SAGE_ERR_BAD_PAGE from the paged-cache entry points,
+ * else SAGE_OK.  With both pending, the second call returns the page error.
+ * Synchronises `stream`.
  */
 SAGE_API sage_status sage_last_device_error(void *stream);
 

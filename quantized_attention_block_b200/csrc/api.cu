@@ -563,18 +563,20 @@ sage_status sage_debug_qk_nvfp4(const sage_nvfp4_view* view, const sage_params* 
 
 sage_status sage_last_device_error(void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  unsigned int err = 0, page = 0, zero = 0;
+  unsigned int err = 0, page = 0;
+  const unsigned int zero = 0;
   if (cudaMemcpyFromSymbolAsync(&err, sage::g_device_error, sizeof(err), 0, cudaMemcpyDeviceToHost, st) !=
-      cudaSuccess)
+          cudaSuccess ||
+      cudaMemcpyFromSymbolAsync(&page, sage::g_page_error, sizeof(page), 0, cudaMemcpyDeviceToHost, st) !=
+          cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
     return SAGE_ERR_CUDA;
-  if (cudaMemcpyToSymbolAsync(sage::g_device_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st) !=
-      cudaSuccess)
+  // only what is reported is cleared: with both pending, the page error is left for the next call
+  if (err != 0 && cudaMemcpyToSymbolAsync(sage::g_device_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st) !=
+                      cudaSuccess)
     return SAGE_ERR_CUDA;
-  if (cudaMemcpyFromSymbolAsync(&page, sage::g_page_error, sizeof(page), 0, cudaMemcpyDeviceToHost, st) !=
-      cudaSuccess)
-    return SAGE_ERR_CUDA;
-  if (cudaMemcpyToSymbolAsync(sage::g_page_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st) !=
-      cudaSuccess)
+  if (err == 0 && page != 0 &&
+      cudaMemcpyToSymbolAsync(sage::g_page_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st) != cudaSuccess)
     return SAGE_ERR_CUDA;
   if (cudaStreamSynchronize(st) != cudaSuccess) return SAGE_ERR_CUDA;
   return err != 0 ? SAGE_ERR_TIMEOUT : page != 0 ? SAGE_ERR_BAD_PAGE : SAGE_OK;

@@ -171,3 +171,13 @@ def test_window_nan_in_every_value_of_a_channel(short_waits, d, dtype, window, s
     for h in (0, 17, 31):
         ref, tol = some_rows(q, k, v, 0, h, rows, window, sinks)
         assert_within(got[0, h, rows][..., keep], ref[:, keep], tol[:, keep])
+
+
+# ---------------------------------------------------------------- errors
+def test_a_timeout_does_not_hide_a_bad_page():
+    cache = sage.KVCache.alloc(8, 16, 2, 64, BF)
+    table = torch.full((1, 2), 99, dtype=torch.int32, device="cuda")
+    lens = torch.full((1,), 20, dtype=torch.int32, device="cuda")
+    sage.sage_attn_decode(torch.zeros((1, 4, 64), dtype=BF, device="cuda"), cache, table, lens)
+    assert sage.sage_debug_bounded_wait(2000) == 7
+    assert [sage.sage_last_device_error() for _ in range(2)] == [9, 0]
