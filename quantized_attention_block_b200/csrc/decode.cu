@@ -161,9 +161,10 @@ __device__ __forceinline__ float load16(const void* p, int64_t i, int fp16) {
 template <int D>
 __device__ __forceinline__ void write_lse(const DecodeArgs& a, int b, int hq, float m, float l) {
   const int lane = threadIdx.x & 31;
-  const float lse2 = l > 0.0f || isnan(l) ? m + log2f(l) : -INFINITY;
+  const bool some = l > 0.0f || isnan(l);  // (without a key: -inf, whatever the query of a padded row holds)
+  const float lse2 = some ? m + log2f(l) : -INFINITY;
   float dot = 0.0f;
-  if (a.km && a.lse) {
+  if (a.km && a.lse && some) {
     const float* km = a.km + ((int64_t)b * a.c.H + hq / a.G) * D;
     for (int i = lane; i < D; i += 32) dot += load16(a.q, ((int64_t)b * a.Hq + hq) * D + i, a.q_fp16) * km[i];
 #pragma unroll

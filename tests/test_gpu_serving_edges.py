@@ -181,3 +181,24 @@ def test_a_timeout_does_not_hide_a_bad_page():
     sage.sage_attn_decode(torch.zeros((1, 4, 64), dtype=BF, device="cuda"), cache, table, lens)
     assert sage.sage_debug_bounded_wait(2000) == 7
     assert [sage.sage_last_device_error() for _ in range(2)] == [9, 0]
+
+
+# ---------------------------------------------------------------- padded batches
+@pytest.mark.parametrize("max_pages", [2, 100])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_decode_of_an_empty_sequence_goes_by_its_length_alone(bad, max_pages):
+    """Without a key, o = 0 and lse = -inf, whatever the row's query and km hold; one CTA a row, and split."""
+    cache = sage.KVCache.alloc(8, 16, 2, 64, BF, quantized=True)
+    table = torch.zeros((3, max_pages), dtype=torch.int32, device="cuda")
+    table[1, :2] = torch.tensor([3, 4])
+    lens = torch.tensor([0, 20, 0], dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(0)
+    k, v = (torch.randn((3, 2, 20, 64), generator=g, device="cuda").to(BF) for _ in range(2))
+    sage.sage_kv_append(k, v, cache, table, torch.zeros_like(lens), n_new=lens)
+    q = torch.randn((3, 4, 64), generator=g, device="cuda").to(BF)
+    km = torch.randn((3, 2, 64), generator=g, device="cuda")
+    want = sage.sage_attn_decode_lse(q, cache, table, lens, km=km)
+    q[0], q[2], km[2] = bad, bad, bad
+    o, lse = sage.sage_attn_decode_lse(q, cache, table, lens, km=km)
+    assert (o[[0, 2]] == 0).all() and (lse[[0, 2]] == -math.inf).all()
+    assert torch.equal(o[1], want[0][1]) and torch.equal(lse[1], want[1][1]) and torch.isfinite(lse[1]).all()
