@@ -183,7 +183,8 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const EvictArgs 
   }
   int* kept = a.kept + (int64_t)blockIdx.x * a.keep;
   if (n <= a.keep) {
-    for (int i = tid; i < a.keep; i += kSelThreads) kept[i] = i < n ? i : -1;
+    // (unsigned: the last step may pass 2^31)
+    for (uint32_t i = tid; i < (uint32_t)a.keep; i += kSelThreads) kept[i] = i < (uint32_t)n ? (int)i : -1;
     return;
   }
   const int lo = a.sinks, cand = n - a.recent - lo;  // candidates: tokens lo + [0, cand)

@@ -202,3 +202,25 @@ def test_decode_of_an_empty_sequence_goes_by_its_length_alone(bad, max_pages):
     o, lse = sage.sage_attn_decode_lse(q, cache, table, lens, km=km)
     assert (o[[0, 2]] == 0).all() and (lse[[0, 2]] == -math.inf).all()
     assert torch.equal(o[1], want[0][1]) and torch.equal(lse[1], want[1][1]) and torch.isfinite(lse[1]).all()
+
+
+# ---------------------------------------------------------------- largest arguments
+def test_evict_to_the_largest_budget():
+    """keep = 2^31 - 1: every token stays, the 8 GB of kept end in -1, and nothing before them is written."""
+    keep, page = 2 ** 31 - 1, 1024
+    cache = sage.KVCache.alloc(2, page, 1, 64, BF, track_weight=True)
+    cache.k_pages[0] = torch.randn((1, page, 64), device="cuda").to(BF)
+    table = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    dst = torch.full((1, -(-keep // page)), -1, dtype=torch.int32, device="cuda")
+    dst[0, 0] = 1
+    lens = torch.full((1,), 700, dtype=torch.int32, device="cuda")
+    buf = torch.full((keep + 4097,), 7, dtype=torch.int32, device="cuda")
+    at = 4096 - 3  # (not aligned to more than its type)
+    kept = buf[at:at + keep].view(1, 1, keep)
+    new_lens, _ = sage.sage_kv_evict(cache, table, lens, dst, keep, sinks=4, recent=16, kept=kept)
+    assert new_lens.tolist() == [700]
+    assert torch.equal(kept[0, 0, :700], torch.arange(700, dtype=torch.int32, device="cuda"))
+    assert kept[0, 0, 700:].amin() == -1 == kept[0, 0, 700:].amax()
+    assert (buf[:at] == 7).all() and (buf[at + keep:] == 7).all()
+    assert torch.equal(cache.k_pages[1, 0, :700], cache.k_pages[0, 0, :700])
+    assert not cache.k_pages[1, 0, 700:].any()
