@@ -119,3 +119,32 @@ def test_only_masked_steps_hold_keys_that_a_row_does_not_see():
                     for p in (p0, min(p0 + 127, n - 1)):
                         for j in (k0, k0 + 63):
                             assert j <= p and (w.window == 0 or p - j < w.window or j < w.sinks)
+
+
+# ---------------------------------------------------------------- the order of the items
+def order(B, Hq, Hkv, N, D):
+    """(head, first row) of each item, as the launch and win_item have them, and the heads of a group."""
+    heads, pairs = B * Hq, -(-N // 256)
+    groups = (heads * N * D * 4 // (Hq // Hkv) + (32 << 20) - 1) >> 25
+    groups = min(max(groups, 1), heads)
+    group = -(-heads // groups)
+    out = []
+    for idx in range(heads * pairs):
+        g, at = divmod(idx, group * pairs)
+        here = min(group, heads - g * group)
+        pair, h = divmod(at, here)
+        out.append((g * group + h, 256 * (pairs - 1 - pair)))
+    return out, group
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,N,D", [(1, 11, 11, 8192, 128), (4, 32, 32, 4096, 128), (1, 32, 8, 8192, 128),
+                                          (3, 7, 1, 20000, 64), (2, 5, 5, 100000, 128), (1, 1, 1, 1, 64),
+                                          (1, 3, 3, 70000, 128), (7, 13, 13, 2500, 64)])
+def test_every_item_comes_once_and_a_group_at_a_time(B, Hq, Hkv, N, D):
+    items, group = order(B, Hq, Hkv, N, D)
+    heads, pairs = B * Hq, -(-N // 256)
+    assert sorted(items) == [(h, 256 * p) for h in range(heads) for p in range(pairs)]
+    assert [h // group for h, _ in items] == sorted(h // group for h, _ in items)
+    for g in range(-(-heads // group)):     # a group's heaviest rows first
+        rows = [q0 for h, q0 in items if h // group == g]
+        assert rows == sorted(rows, reverse=True)
