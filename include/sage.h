@@ -428,7 +428,8 @@ typedef struct {
  * number outside [0, n_pages) counts as a page without tokens (nothing is read
  * from it or written to it), a length outside [0, max_pages * page_size] is
  * taken as the nearest bound; both record SAGE_ERR_BAD_PAGE for
- * sage_last_device_error.  Two sequences of a call may share pages that the
+ * sage_last_device_error.  (An n_new outside [0, T] is taken as the nearest
+ * bound, unrecorded.)  Two sequences of a call may share pages that the
  * call only reads.  Only looked-up table entries are read: those of the visible
  * keys (sage_attn_decode), of the new tokens (sage_kv_append).
  */
@@ -462,7 +463,9 @@ typedef struct {
 } sage_decode_params;
 
 /* Bytes of workspace that sage_attn_decode needs (0: invalid arguments).  Goes by sizes, c->weight != NULL and
- * max_pages alone (device data and lengths do not matter). */
+ * max_pages alone (device data and lengths do not matter).  At most 11 MB; with c->weight, 4 more bytes for each
+ * sequence, query head and token that the table (or the window and the sinks) can show: 2.1 GB for 64 sequences, 64
+ * heads and tables for 131072 tokens, so keep max_pages near the lengths then. */
 SAGE_API size_t sage_decode_workspace_bytes(const sage_kv_cache *c, const sage_kv_seqs *s,
                                             const sage_decode_params *p);
 

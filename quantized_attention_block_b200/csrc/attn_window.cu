@@ -33,9 +33,10 @@
 //
 // Bound: the two chains of S, softmax and P V.  A step takes 1880 cycles, 1260 of
 // them products of both row tiles (N = 64 counted at its real rate), 1020
-// exponentials.  B4 H32 N4096 d128, window 1024, 4 sinks: 0.28 ms, 870 TFLOP/s of
-// visible pairs; 32 heads on 8, N8192, window 4096: 0.36 ms, 1150 TFLOP/s, 68% of
-// a large cuBLAS product.
+// exponentials.  B4 H32 N4096 d128, window 1024, 4 sinks: 0.28 ms, 860 TFLOP/s of
+// visible pairs; 32 heads on 8, N8192, window 4096: 0.36 ms, 1150 TFLOP/s, 69% of
+// a large cuBLAS product: a few hundred calls from idle.  Called for seconds, 0.33
+// and 0.42 ms: the power limit then holds the SM clock at 1575 and 1650 MHz of 1965.
 //
 // Keys a row does not see are -inf before the maximum, so their weights are
 // exact zeros; a NaN or infinity in such a key's V still makes 0 x inf = NaN in

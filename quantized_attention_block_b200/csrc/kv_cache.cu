@@ -272,8 +272,9 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const EvictArgs 
 
 // Moves the rows that stay.  One row of K or V is ROW_BYTES / 16 lanes; a thread
 // has its 16 bytes of K and V of two rows in flight.  More are slower, not faster
-// (192 us in all with two, 246 with four, 321 with eight for 128 rows of up to
-// 12288 tokens), and so are accesses that stay in L2 (212 us).
+// (192 us on the device for the whole call with two, 246 with four, 321 with eight,
+// for 128 rows of up to 12288 tokens), and so are accesses that stay in L2 (212 us).
+// (With the weights and scales moved as below, 180.)
 // (kept with plain loads: the selection may still write it when this kernel
 // starts, and the non-coherent ones are for data that no kernel writes meanwhile.)
 constexpr int kMoveThreads = 128, kMoveRows = 2;
@@ -288,8 +289,8 @@ __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictArgs a
   const int lane = threadIdx.x % L;
   const int page = 1 << a.c.page_log2;
   const int esize = a.quantized ? 1 : 2;
-  // weights and scales, a thread a row (a lane of each row's in the loop below: 198 us against 190 for 128 rows of up
-  // to 12288 tokens; bad pages are recorded there)
+  // weights and scales, a thread a row (by a lane of each row's in the loop below, 198 us a call against 190 for 128
+  // rows of up to 12288 tokens; on the device 192 and 180; bad pages are recorded there)
   constexpr int ROWS = PASS * kMoveRows;  // of the CTA at a time
   static_assert(ROWS <= kMoveThreads, "a thread a row");
   for (int i = blockIdx.y * ROWS + threadIdx.x; threadIdx.x < ROWS && i < n; i += gridDim.y * ROWS) {
