@@ -2,13 +2,15 @@
 replays than the tests of their masks: groups of heads in the sliding-window
 kernel, joins of many heads, wide groups over long rows, weights gathered by
 replayed graphs."""
+import math
+
 import pytest
 import torch
 
 from quantized_attention_block_b200 import sage
 
-from serving_ref import Paged, assert_within, decode_ref
-from test_gpu_serving import bits, check_decode, no_device_error  # noqa: F401
+from serving_ref import Paged, assert_within, decode_ref, window_ref
+from test_gpu_serving import bits, check_decode, no_device_error, window_inputs  # noqa: F401
 from test_gpu_serving_edges import many_items, some_rows
 from test_window_again import order
 
@@ -78,3 +80,36 @@ def test_replayed_graphs_gather_weights(longest, window):
                 # as in check_decode, a replay after the other
                 tol[pid, :, r] += (2.1 * err + 2.0 ** -19) * p + 4 * 2.0 ** -23 * want[pid, :, r].abs()
         assert_within(cache.weight, want, tol)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (1, 2), (70, 3), (130, 64), (200, 130), (64, 65), (500, 1)])
+@pytest.mark.parametrize("d,dtype,layout", [(64, FP, "NHD"), (128, BF, "HND"), (128, FP, "NHD")])
+def test_window_bad_values_in_many_places(d, dtype, layout, window, sinks):
+    """NaN and infinities at random in V: a channel of a row is not finite if the row sees one there, and what it would
+    be without them else; padded batches, grouped heads."""
+    B, Hq, Hkv, N, lens = 3, 4, 2, 700, [700, 0, 431]
+    q, k, v = window_inputs(B, Hq, Hkv, N, d, dtype, seed=window)
+    ref, rl, to, tl = window_ref(q, k, v, window, sinks, lens)
+    g = torch.Generator().manual_seed(sinks)
+    bad = torch.zeros(v.shape, dtype=torch.bool)
+    for _ in range(12):
+        b, h, j, c = (int(torch.randint(0, n, (1,), generator=g)) for n in (B, Hkv, N, d))
+        bad[b, h, j, c] = True
+        v[b, h, j, c] = (math.nan, math.inf, -math.inf)[j % 3]
+    for b, n in enumerate(lens):
+        for x in (q, k, v):
+            x[b, :, n:] = math.nan
+        bad[b, :, n:] = False
+    x = [(t if layout == "HND" else t.transpose(1, 2)).contiguous().cuda() for t in (q, k, v)]
+    o, lse = sage.sage_attn_window_fwd_lse(*x, window=window, sinks=sinks, lens=torch.tensor(lens).int().cuda(),
+                                           tensor_layout=layout)
+    o = (o if layout == "HND" else o.transpose(1, 2)).cpu()
+    p, j = torch.arange(N)[:, None], torch.arange(N)[None]
+    see = (j <= p) & ((p - j < window) | (j < sinks) | (window == 0))
+    hit = (see.double() @ bad.double() > 0).repeat_interleave(Hq // Hkv, 1)
+    live = ~torch.isnan(ref)
+    assert not torch.isfinite(o[hit & live]).any()
+    assert_within(o[~hit & live], ref[~hit & live], to[~hit & live], "o")
+    assert (o[~live] == 0).all()
+    rows = ~torch.isnan(rl)
+    assert_within(lse.cpu()[rows], rl[rows], tl[rows], "lse")
